@@ -8,6 +8,7 @@ of the same name.  All arithmetic runs in the library's kernels.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -404,3 +405,155 @@ def butterfly_apply_tc(x, radices, blocks, axis: int = 1, transpose: bool = Fals
          ctypes.cast(ng, ctypes.c_void_p), int(bool(transpose)), axis, _ptr(ws),
          0 if ws is None else ws.numel() * ws.element_size(), _stream(x.device))
     return out
+
+
+# ---------------------------------------------------------------------------
+# Rotated key/value cache
+# ---------------------------------------------------------------------------
+_KV = struct.Struct("@12Q4q8i")  # struct hit_kv
+
+
+def kv_cache_shapes(pages: int, page_size: int, kv_heads: int, head_dim: int, bits: int):
+    """Shapes of the codes (uint8) and scales (float32) of a cache of `pages` pages; keys and values have one of each."""
+    return (pages, kv_heads, page_size, head_dim * bits // 8), (pages, kv_heads, page_size)
+
+
+def _kv(d, dev, tokens, k_codes, k_scales, v_codes, v_scales, page_table, lens, cu, k_signs, v_signs, inv_freq=None,
+        interleaved=False, positions=None, rope_axis=None):
+    """The packed struct hit_kv of a call, after checking its tensors against one another."""
+    u8, f32, i32 = torch.uint8, torch.float32, torch.int32
+    shape = k_codes.shape
+    if k_codes.dim() != 4 or k_codes.dtype != u8 or v_codes.dtype != u8 or v_codes.shape != shape:
+        raise ValueError("k_codes and v_codes must be uint8 [pages, kv_heads, page_size, head_dim * bits / 8]")
+    if k_scales.dtype != f32 or v_scales.dtype != f32 or k_scales.shape != shape[:3] or v_scales.shape != shape[:3]:
+        raise ValueError("k_scales and v_scales must be float32 [pages, kv_heads, page_size]")
+    if page_table.dim() != 2 or page_table.dtype != i32 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table must be int32 [seqs, pages of a sequence] with unit stride along a row")
+    seqs, max_pages = page_table.shape
+    if lens.dtype != i32 or lens.shape != (seqs,) or cu.dtype != i32 or cu.shape != (seqs + 1,):
+        raise ValueError("lens must be int32 [seqs] and cu int32 [seqs + 1]")
+    n_freq, axes, ld_pos = 0, 1, 0
+    tensors = [k_codes, k_scales, v_codes, v_scales, lens, cu]
+    for s in (k_signs, v_signs):
+        if s is not None:
+            if s.dtype != torch.int8 or s.shape != (d,):
+                raise ValueError("k_signs and v_signs must be int8 [head_dim]")
+            tensors.append(s)
+    if inv_freq is not None:
+        if inv_freq.dtype != f32 or inv_freq.dim() != 1:
+            raise ValueError("inv_freq must be a float32 vector")
+        tensors.append(inv_freq)
+        n_freq = inv_freq.shape[0]
+        if positions is not None:
+            if positions.dtype != i32 or positions.dim() not in (1, 2) or positions.shape[-1] != tokens:
+                raise ValueError("positions must be int32 [tokens] or [axes, tokens]")
+            tensors.append(positions)
+            axes, ld_pos = (positions.shape[0] if positions.dim() == 2 else 1), tokens
+            if rope_axis is not None:
+                if rope_axis.dtype != torch.int8 or rope_axis.shape != (n_freq,):
+                    raise ValueError("rope_axis must be int8, one axis for each frequency")
+                tensors.append(rope_axis)
+            elif axes != 1:
+                raise ValueError("several position axes need rope_axis")
+        elif rope_axis is not None:
+            raise ValueError("rope_axis needs positions")
+    elif positions is not None or rope_axis is not None:
+        raise ValueError("positions and rope_axis need inv_freq")
+    for t in tensors:
+        if t.device != dev or not t.is_contiguous():
+            raise ValueError("the cache, lens, cu, signs and positions must be contiguous, all on one CUDA device")
+    if page_table.device != dev:
+        raise ValueError("page_table must be on the cache's device")
+    ptr = [0 if t is None else t.data_ptr()
+           for t in (k_codes, k_scales, v_codes, v_scales, page_table, lens, cu, k_signs, v_signs, inv_freq, positions,
+                     rope_axis)]
+    bits = shape[3] * 8 // d
+    if shape[3] * 8 != d * bits:
+        raise ValueError("the codes' last dimension does not fit head_dim")
+    return _KV.pack(*ptr, shape[0], shape[2], page_table.stride(0) if seqs > 1 else max_pages, ld_pos, shape[1], d, bits,
+                    seqs, max_pages, n_freq, axes, int(bool(interleaved)))
+
+
+def _kv_dense(t, name, heads=None):
+    _cuda(t, name)
+    if t.dim() != 3 or t.stride(2) != 1 or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [tokens, heads, head_dim] with unit stride inside a head")
+    return t
+
+
+def _kv_call(dev, name, *args):
+    """The call on the tensors' device (it need not be the current one) and its current stream."""
+    if dev.index == torch.cuda.current_device():
+        call(name, *args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            call(name, *args, torch.cuda.current_stream(dev).cuda_stream)
+
+
+def rht_kv_append(k, v, k_codes, k_scales, v_codes, v_scales, page_table, lens, cu, k_signs=None, v_signs=None,
+                  inv_freq=None, interleaved: bool = False, positions=None, rope_axis=None) -> None:
+    """Put k and v [tokens, kv_heads, head_dim] into the paged cache, in place: rotary turn (keys), rotation
+    H diag(signs) / sqrt(head_dim), absmax codes with one scale per head vector.
+
+    Sequence s owns tokens cu[s] .. cu[s + 1]; they are the last of its lens[s] positions, and position p lives in
+    page page_table[s, p // page_size].  The cache's tensors have kv_cache_shapes(); 4 or 8 bits go by their shape.
+    positions (int32 [tokens] or [axes, tokens], with rope_axis int8 [n_freq]) replaces the sequence positions."""
+    _kv_dense(k, "k")
+    _kv_dense(v, "v", k.shape[1])
+    if v.shape != k.shape or v.dtype != k.dtype or v.device != k.device:
+        raise ValueError("k and v must have the same shape, dtype and device")
+    if k_codes.shape[1] != k.shape[1]:
+        raise ValueError("k's heads are not the cache's")
+    dev, n = k.device, k.shape[0]
+    kv = _kv(k.shape[2], dev, n, k_codes, k_scales, v_codes, v_scales, page_table, lens, cu, k_signs, v_signs, inv_freq,
+             interleaved, positions, rope_axis)
+    _kv_call(dev, "rht_kv_append", kv, k.data_ptr(), v.data_ptr(), n, k.stride(0), k.stride(1), v.stride(0),
+             v.stride(1), _dt(k.dtype))
+
+
+def rht_kv_attention(q, k_codes, k_scales, v_codes, v_scales, page_table, lens, cu, k_signs=None, v_signs=None,
+                     inv_freq=None, interleaved: bool = False, positions=None, rope_axis=None,
+                     sm_scale: float | None = None, causal: bool = True, window: int = 0, max_new: int | None = None,
+                     out=None, workspace=None):
+    """Attention of q [tokens, heads, head_dim] over the cached keys and values of its tokens' sequences.
+
+    q is turned and rotated as the keys were; the result is rotated back.  A token at position p sees the cached
+    positions up to p (all of them with causal=False; the last `window` ones with window > 0).  max_new bounds the
+    tokens of one sequence (default: all of them).  out may be float32 or bfloat16 (default: q's type)."""
+    _kv_dense(q, "q")
+    dev, (n, heads, d) = q.device, q.shape
+    if out is None:
+        out = torch.empty((n, heads, d), dtype=q.dtype, device=dev)
+    else:
+        _kv_dense(out, "out")
+        if out.shape != q.shape or out.device != dev:
+            raise ValueError("out must have q's shape and device")
+    kv = _kv(d, dev, n, k_codes, k_scales, v_codes, v_scales, page_table, lens, cu, k_signs, v_signs, inv_freq,
+             interleaved, positions, rope_axis)
+    need = load().rht_kv_workspace_bytes(heads, k_codes.shape[1], d)
+    ws = workspace
+    if ws is None and need > 0:
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    _kv_call(dev, "rht_kv_attention", kv, q.data_ptr(), out.data_ptr(), n, heads, q.stride(0), q.stride(1),
+             out.stride(0), out.stride(1), _dt(q.dtype), _dt(out.dtype),
+             float(d ** -0.5 if sm_scale is None else sm_scale), int(bool(causal)), int(window),
+             int(max(n, 1) if max_new is None else max_new), _ptr(ws),
+             0 if ws is None else ws.numel() * ws.element_size())
+    return out
+
+
+def rht_kv_read(k_codes, k_scales, v_codes, v_scales, page_table, lens, cu, rows: int, head_dim: int, k_signs=None,
+                v_signs=None, out_dtype=torch.bfloat16, k_out=None, v_out=None):
+    """What the cache stands for at the call's tokens: (k, v), each [rows, kv_heads, head_dim], rotated back.
+
+    Sequence s owns rows cu[s] .. cu[s + 1], the last of its lens[s] positions; keys keep their rotary turn."""
+    dev = _cuda(k_codes, "k_codes").device
+    shape = (rows, k_codes.shape[1], head_dim)
+    k = torch.empty(shape, dtype=out_dtype, device=dev) if k_out is None else _kv_dense(k_out, "k_out")
+    v = torch.empty(shape, dtype=k.dtype, device=dev) if v_out is None else _kv_dense(v_out, "v_out")
+    if k.shape != shape or v.shape != shape or k.dtype != v.dtype or k.device != dev or v.device != dev:
+        raise ValueError("k_out and v_out must be [rows, kv_heads, head_dim] of one dtype on the cache's device")
+    kv = _kv(head_dim, dev, rows, k_codes, k_scales, v_codes, v_scales, page_table, lens, cu, k_signs, v_signs)
+    _kv_call(dev, "rht_kv_read", kv, k.data_ptr(), v.data_ptr(), rows, k.stride(0), k.stride(1), v.stride(0),
+             v.stride(1), _dt(k.dtype))
+    return k, v

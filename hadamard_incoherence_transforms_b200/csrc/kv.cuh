@@ -1,0 +1,174 @@
+// Shared pieces of the rotated key/value cache kernels: where a token lives,
+// rotary angles, and the head rotation H_d diag(s) / sqrt(d) of a vector held
+// by a few lanes.
+#pragma once
+#include "device.cuh"
+#include "kv.h"
+
+namespace hit {
+
+// A token's sequence, position and place.
+struct KvToken {
+  int seq;       // -1: the token belongs to no sequence
+  int64_t pos;   // position in the sequence (may be negative)
+  int64_t slot;  // page * kv_heads * page_size + offset of head 0, or -1
+};
+
+// Number of i in [0, seqs] with cu[i] <= t, found by the whole warp: every
+// step probes 32 evenly spaced entries at once, so that the chain of dependent
+// loads is log32(seqs) long.  For an ascending cu this is the token's sequence
+// plus one; for any other contents it is some value in [0, seqs + 1].
+__device__ __forceinline__ int kv_count_le(const int32_t* __restrict__ cu, int seqs, int64_t t, int lane) {
+  int lo = 0, n = seqs + 1;  // the count is in [lo, lo + n]
+  while (n > 0) {
+    const int step = (n + 31) / 32;
+    const int i = lane * step;  // probes lo + i, the first of its piece
+    const bool le = i < n && __ldg(cu + lo + i) <= t;
+    const int k = __popc(__ballot_sync(0xffffffffu, le));
+    if (k == 0) return lo;
+    lo += (k - 1) * step + 1;
+    const int left = n - ((k - 1) * step + 1);
+    n = left < step - 1 ? left : step - 1;
+  }
+  return lo;
+}
+
+// Slot of position p of sequence s, or -1 where it does not exist.
+__device__ __forceinline__ int64_t kv_slot(const KvArgs& a, int s, int64_t p) {
+  if (p < 0) return -1;
+  const int64_t c = p >> a.log_page;
+  if (c >= a.max_pages) return -1;
+  const int64_t page = __ldg(a.table + int64_t(s) * a.ld_table + c);
+  if (page < 0 || page >= a.pages) return -1;
+  return ((page * a.hk) << a.log_page) + (p & ((int64_t(1) << a.log_page) - 1));
+}
+
+// Token t of the call (whole warp, same t).
+__device__ __forceinline__ KvToken kv_token(const KvArgs& a, int64_t t, int lane) {
+  KvToken k{-1, 0, -1};
+  const int c = kv_count_le(a.cu, a.seqs, t, lane);
+  if (c < 1 || c > a.seqs) return k;
+  const int s = c - 1;
+  const int64_t b = __ldg(a.cu + s), e = __ldg(a.cu + s + 1);
+  if (t < b || t >= e) return k;
+  k.seq = s;
+  k.pos = int64_t(__ldg(a.lens + s)) - (e - b) + (t - b);
+  k.slot = kv_slot(a, s, k.pos);
+  return k;
+}
+
+// Cosine and sine of pair j of token t at sequence position pos.  The product
+// is formed and reduced to a fraction of a turn in fp64 (a position of 10^6
+// would leave fp32 no correct digits), the functions are taken in fp32.
+__device__ __forceinline__ float2 kv_angle(const KvArgs& a, int64_t t, int64_t pos, int j) {
+  int64_t p = pos;
+  if (a.positions != nullptr) {
+    const int ax = a.rope_axis != nullptr ? __ldg(a.rope_axis + j) : 0;
+    if (ax < 0 || ax >= a.rope_axes) return make_float2(1.0f, 0.0f);
+    p = __ldg(a.positions + int64_t(ax) * a.ld_pos + t);
+  }
+  const double turns = double(p) * double(__ldg(a.inv_freq + j)) * 0.15915494309189533577;
+  const float frac = float(2.0 * (turns - rint(turns)));
+  float s, c;
+  sincospif(frac, &s, &c);
+  return make_float2(c, s);
+}
+
+// ---------------------------------------------------------------------------
+// A head vector of D elements on LPV = D / 32 neighbouring lanes: lane l of
+// them holds the four 8-element chunks l, l + LPV, l + 2 LPV, l + 3 LPV
+// (x[8 c + e] = element 8 (c LPV + l) + e), so that loads of a chunk are
+// coalesced over the lanes and five of the log2 D Hadamard stages are
+// register stages.
+// ---------------------------------------------------------------------------
+template <int D>
+struct KvLanes {
+  static constexpr int LPV = D / 32;
+  static constexpr int LOG = LPV == 2 ? 1 : LPV == 4 ? 2 : 3;
+};
+
+// Unnormalised Hadamard transform of the vector.
+template <int D>
+__device__ __forceinline__ void kv_hadamard(float (&x)[32], int l) {
+  reg_stages<32, 0, 5>(x);
+#pragma unroll
+  for (int b = 0; b < KvLanes<D>::LOG; ++b) shfl_stage<32>(x, b, (l >> b) & 1);
+}
+
+// x <- diag(signs) x
+template <int D>
+__device__ __forceinline__ void kv_signs(float (&x)[32], const int8_t* __restrict__ signs, int l) {
+  if (signs == nullptr) return;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int q = c * KvLanes<D>::LPV + l;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t b = uint32_t(uint8_t(__ldg(signs + 8 * q + e)));
+      x[8 * c + e] = __uint_as_float(__float_as_uint(x[8 * c + e]) ^ ((b << 24) & 0x80000000u));
+    }
+  }
+}
+
+// Eight consecutive elements as fp32.
+template <bool F32>
+__device__ __forceinline__ void kv_load8(const void* p, int64_t at, float* x) {
+  if constexpr (F32) {
+    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+    const float4 a = __ldg(s), b = __ldg(s + 1);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  } else {
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at));
+    bf16x2_to_f32(w.x, x[0], x[1]);
+    bf16x2_to_f32(w.y, x[2], x[3]);
+    bf16x2_to_f32(w.z, x[4], x[5]);
+    bf16x2_to_f32(w.w, x[6], x[7]);
+  }
+}
+template <bool F32>
+__device__ __forceinline__ void kv_store8(void* p, int64_t at, const float* x) {
+  if constexpr (F32) {
+    float4* d = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
+    d[0] = make_float4(x[0], x[1], x[2], x[3]);
+    d[1] = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + at) =
+        make_uint4(f32_to_bf16x2(x[0], x[1]), f32_to_bf16x2(x[2], x[3]), f32_to_bf16x2(x[4], x[5]),
+                   f32_to_bf16x2(x[6], x[7]));
+  }
+}
+
+// The rotary turn of a vector whose elements start at p + at; cs holds the
+// token's (cos, sin) pairs.
+template <int D, bool F32>
+__device__ __forceinline__ void kv_rope(float (&x)[32], const void* p, int64_t at, const float2* cs, int n_freq,
+                                        bool interleaved, int l) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int i0 = 8 * (c * KvLanes<D>::LPV + l);
+    if (i0 >= 2 * n_freq) continue;
+    float* v = x + 8 * c;
+    if (interleaved) {
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        const float2 t = cs[(i0 + e) / 2];
+        const float u = v[e], w = v[e + 1];
+        v[e] = u * t.x - w * t.y;
+        v[e + 1] = u * t.y + w * t.x;
+      }
+    } else {
+      // the partner chunk lies n_freq elements on or back (n_freq % 8 == 0)
+      const bool low = i0 < n_freq;
+      float o[8];
+      kv_load8<F32>(p, at + (low ? i0 + n_freq : i0 - n_freq), o);
+      const int j0 = low ? i0 : i0 - n_freq;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float2 t = cs[j0 + e];
+        v[e] = low ? v[e] * t.x - o[e] * t.y : o[e] * t.y + v[e] * t.x;
+      }
+    }
+  }
+}
+
+}  // namespace hit

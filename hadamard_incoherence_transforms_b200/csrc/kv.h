@@ -1,0 +1,51 @@
+// Launcher interface of the rotated key/value cache (host-side C++).
+#pragma once
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace hit {
+
+// The cache, the call's sequences and the rotary positions (see hit.h).
+struct KvArgs {
+  uint8_t* k_codes = nullptr;
+  uint8_t* v_codes = nullptr;
+  float* k_scales = nullptr;
+  float* v_scales = nullptr;
+  const int32_t* table = nullptr;
+  const int32_t* lens = nullptr;
+  const int32_t* cu = nullptr;
+  const int8_t* k_signs = nullptr;
+  const int8_t* v_signs = nullptr;
+  const float* inv_freq = nullptr;
+  const int32_t* positions = nullptr;
+  const int8_t* rope_axis = nullptr;
+  int64_t pages = 0, ld_table = 0, ld_pos = 0;
+  int64_t tokens = 0;
+  int hk = 1, log_page = 0, seqs = 0, max_pages = 0;
+  int n_freq = 0, interleaved = 0, rope_axes = 1;
+  int head_dim = 0, bits = 0;
+};
+
+// Dense keys and values (either may be NULL for reading).
+struct KvDense {
+  const void* k = nullptr;
+  const void* v = nullptr;
+  int64_t k_ts = 0, k_hs = 0, v_ts = 0, v_hs = 0;
+};
+cudaError_t launch_kv_append(const KvArgs& a, const KvDense& x, int dt, cudaStream_t st);
+cudaError_t launch_kv_read(const KvArgs& a, const KvDense& y, int dt, cudaStream_t st);
+
+struct KvAttn {
+  const void* q = nullptr;
+  void* out = nullptr;
+  int64_t q_ts = 0, q_hs = 0, o_ts = 0, o_hs = 0;
+  int heads = 0, q_f32 = 0, o_f32 = 0, causal = 1;
+  float scale = 1.0f;
+  int64_t window = 0;
+  int64_t max_new = 1;
+  void* ws = nullptr;
+};
+cudaError_t launch_kv_attention(const KvArgs& a, const KvAttn& t, cudaStream_t st);
+
+}  // namespace hit

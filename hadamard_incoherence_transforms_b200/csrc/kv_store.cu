@@ -1,0 +1,250 @@
+// Appending to and reading from the rotated key/value cache.
+//
+// Append: per (token, head) vector u = H diag(s) rope(x) / sqrt(d), absmax
+// RTN with one scale per vector, codes and scale to the token's slot.  Read:
+// R^-1 (q s) = diag(s) H (q s) / sqrt(d).  Both touch every byte once and do
+// log2 d + a few operations per element, so memory bounds them for long calls
+// and latency for short ones.  A vector sits on d / 32 lanes (32 elements
+// each), which leaves only 1 to 3 of the 6 to 8 Hadamard stages to shuffles.
+#include "kv.cuh"
+
+#include <algorithm>
+
+namespace hit {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxTile = 16;  // tokens per CTA
+
+// Eight stored codes of t = y / s, by the correctly rounded quotient: q0 = y r
+// with r = RN(1/s), one correction step (exact remainder), and the code in the
+// low byte of t + 1.5 * 2^23 + 2^(b-1) (ties to even).
+__device__ __forceinline__ uint32_t kv_code(float y, float s, float r, float magic) {
+  const float q0 = y * r;
+  const float e = fmaf(-s, q0, y);
+  return __float_as_uint(fmaf(e, r, q0) + magic);
+}
+
+// Codes of the vector x (already normalised) and its scale.  All LPV lanes of
+// the vector call it together; the absmax is taken over bit patterns, where a
+// NaN is above everything, so that it reaches the scale.
+template <int D, int BITS>
+__device__ __forceinline__ float kv_quantize(float (&x)[32], uint32_t (&w)[4 * BITS / 4]) {
+  constexpr int QMAX = (1 << (BITS - 1)) - 1;
+  constexpr float MAGIC = 12582912.0f + float(1 << (BITS - 1));
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
+#pragma unroll
+  for (int b = 0; b < KvLanes<D>::LOG; ++b) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1 << b));
+  const float a = __uint_as_float(m);
+  float s = __fdiv_rn(a, float(QMAX));
+  if (m >= 0x7f800000u) s = __uint_as_float(0x7fc00000u);
+  uint32_t u[32];
+  if (a > 7.9e-31f && a < 1.2e30f) {  // quotient, remainder and reciprocal stay normal
+    const float r = __frcp_rn(s);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) u[i] = kv_code(x[i], s, r, MAGIC);
+  } else {
+    const bool live = s > 0.0f;  // false for s = 0 and for NaN
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const float t = live ? fminf(fmaxf(__fdiv_rn(x[i], s), -float(QMAX)), float(QMAX)) : 0.0f;
+      u[i] = __float_as_uint(t + MAGIC);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    if constexpr (BITS == 4) {
+      w[c] = pack4x8(u + 8 * c);
+    } else {
+      w[2 * c] = low_bytes4(u[8 * c], u[8 * c + 1], u[8 * c + 2], u[8 * c + 3]);
+      w[2 * c + 1] = low_bytes4(u[8 * c + 4], u[8 * c + 5], u[8 * c + 6], u[8 * c + 7]);
+    }
+  }
+  return s;
+}
+
+struct Tile {
+  KvToken tok[kMaxTile];
+};
+
+template <int D, int BITS, bool F32>
+__global__ void __launch_bounds__(kThreads) k_kv_append(const KvArgs a, const KvDense x, int tile, float norm) {
+  constexpr int LPV = KvLanes<D>::LPV;
+  extern __shared__ float2 cs[];  // [tile][n_freq]
+  __shared__ Tile tl;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  const int64_t t0 = int64_t(blockIdx.x) * tile;
+  const int nt = int(min(int64_t(tile), a.tokens - t0));
+  for (int j = warp; j < nt; j += nw) {
+    const KvToken k = kv_token(a, t0 + j, lane);
+    if (lane == 0) tl.tok[j] = k;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < nt * a.n_freq; i += blockDim.x) {
+    const int j = i / a.n_freq, f = i - j * a.n_freq;
+    if (tl.tok[j].slot >= 0) cs[i] = kv_angle(a, t0 + j, tl.tok[j].pos, f);
+  }
+  __syncthreads();
+  const int l = threadIdx.x % LPV;
+  const int vectors = nt * 2 * a.hk;
+  const int per = blockDim.x / LPV;
+  for (int v0 = 0; v0 < vectors; v0 += per) {  // every lane stays in the loop for the shuffles
+    const int v = v0 + int(threadIdx.x) / LPV;
+    const bool in = v < vectors;
+    const int j = in ? v / (2 * a.hk) : 0;
+    const int r = in ? v - j * 2 * a.hk : 0;
+    const bool is_v = r >= a.hk;
+    const int h = is_v ? r - a.hk : r;
+    const int64_t slot = tl.tok[j].slot;
+    const bool live = in && slot >= 0;
+    float y[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) y[i] = 0.0f;
+    if (live) {
+      const void* src = is_v ? x.v : x.k;
+      const int64_t at = (t0 + j) * (is_v ? x.v_ts : x.k_ts) + h * (is_v ? x.v_hs : x.k_hs);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) kv_load8<F32>(src, at + 8 * (c * LPV + l), y + 8 * c);
+      if (!is_v && a.n_freq > 0) kv_rope<D, F32>(y, src, at, cs + j * a.n_freq, a.n_freq, a.interleaved, l);
+      kv_signs<D>(y, is_v ? a.v_signs : a.k_signs, l);
+    }
+    kv_hadamard<D>(y, l);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) y[i] *= norm;
+    uint32_t w[4 * BITS / 4];
+    const float s = kv_quantize<D, BITS>(y, w);
+    if (live) {
+      const int64_t vec = slot + (int64_t(h) << a.log_page);
+      uint8_t* dst = (is_v ? a.v_codes : a.k_codes) + vec * (D * BITS / 8);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if constexpr (BITS == 4)
+          reinterpret_cast<uint32_t*>(dst)[c * LPV + l] = w[c];
+        else
+          reinterpret_cast<uint2*>(dst)[c * LPV + l] = make_uint2(w[2 * c], w[2 * c + 1]);
+      }
+      if (l == 0) (is_v ? a.v_scales : a.k_scales)[vec] = s;
+    }
+  }
+}
+
+template <int D, int BITS, bool F32>
+__global__ void __launch_bounds__(kThreads) k_kv_read(const KvArgs a, const KvDense y, int tile, float norm) {
+  constexpr int LPV = KvLanes<D>::LPV;
+  constexpr float MAGIC = 8388608.0f + float(1 << (BITS - 1));
+  __shared__ Tile tl;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  const int64_t t0 = int64_t(blockIdx.x) * tile;
+  const int nt = int(min(int64_t(tile), a.tokens - t0));
+  for (int j = warp; j < nt; j += nw) {
+    const KvToken k = kv_token(a, t0 + j, lane);
+    if (lane == 0) tl.tok[j] = k;
+  }
+  __syncthreads();
+  const int l = threadIdx.x % LPV;
+  const int vectors = nt * 2 * a.hk;
+  const int per = blockDim.x / LPV;
+  for (int v0 = 0; v0 < vectors; v0 += per) {
+    const int v = v0 + int(threadIdx.x) / LPV;
+    const bool in = v < vectors;
+    const int j = in ? v / (2 * a.hk) : 0;
+    const int r = in ? v - j * 2 * a.hk : 0;
+    const bool is_v = r >= a.hk;
+    const int h = is_v ? r - a.hk : r;
+    void* dst = const_cast<void*>(is_v ? y.v : y.k);
+    const bool owned = in && dst != nullptr && tl.tok[j].seq >= 0;
+    const int64_t slot = tl.tok[j].slot;
+    float z[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) z[i] = 0.0f;
+    if (owned && slot >= 0) {
+      const int64_t vec = slot + (int64_t(h) << a.log_page);
+      const uint8_t* src = (is_v ? a.v_codes : a.k_codes) + vec * (D * BITS / 8);
+      const float s = (is_v ? a.v_scales : a.k_scales)[vec] * norm;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t w[2];
+        if constexpr (BITS == 4) {
+          w[0] = reinterpret_cast<const uint32_t*>(src)[c * LPV + l];
+        } else {
+          const uint2 t = reinterpret_cast<const uint2*>(src)[c * LPV + l];
+          w[0] = t.x, w[1] = t.y;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          z[8 * c + e] = (__uint_as_float(0x4B000000u | code_at<BITS>(w, e)) - MAGIC) * s;
+      }
+    }
+    kv_hadamard<D>(z, l);
+    if (owned) {
+      kv_signs<D>(z, is_v ? a.v_signs : a.k_signs, l);
+      const int64_t at = (t0 + j) * (is_v ? y.v_ts : y.k_ts) + h * (is_v ? y.v_hs : y.k_hs);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) kv_store8<F32>(dst, at + 8 * (c * LPV + l), z + 8 * c);
+    }
+  }
+}
+
+// Tokens per CTA: one while the tokens do not fill the GPU twice, more after
+// that (angles and places of neighbouring tokens are then found together).
+int pick_tile(int64_t tokens) {
+  const int64_t per = tokens / (2 * 148);
+  return int(std::min<int64_t>(kMaxTile, std::max<int64_t>(1, per)));
+}
+int pick_threads(int tile, int hk, int lpv) {
+  const int64_t want = int64_t(tile) * 2 * hk * lpv;
+  return int(std::min<int64_t>(kThreads, (want + 31) / 32 * 32));
+}
+float norm_of(int d) { return d == 64 ? 0.125f : d == 256 ? 0.0625f : 0.08838834764831845f; }
+
+template <typename F>
+cudaError_t by_format(const KvArgs& a, int dt, F f) {
+  const bool f32 = dt == 0;
+  if (a.head_dim == 64)
+    return a.bits == 4 ? (f32 ? f.template go<64, 4, true>() : f.template go<64, 4, false>())
+                       : (f32 ? f.template go<64, 8, true>() : f.template go<64, 8, false>());
+  if (a.head_dim == 128)
+    return a.bits == 4 ? (f32 ? f.template go<128, 4, true>() : f.template go<128, 4, false>())
+                       : (f32 ? f.template go<128, 8, true>() : f.template go<128, 8, false>());
+  return a.bits == 4 ? (f32 ? f.template go<256, 4, true>() : f.template go<256, 4, false>())
+                     : (f32 ? f.template go<256, 8, true>() : f.template go<256, 8, false>());
+}
+
+struct Append {
+  const KvArgs& a;
+  const KvDense& x;
+  cudaStream_t st;
+  template <int D, int BITS, bool F32>
+  cudaError_t go() {
+    const int tile = pick_tile(a.tokens);
+    const unsigned grid = unsigned((a.tokens + tile - 1) / tile);
+    const int threads = pick_threads(tile, a.hk, D / 32);
+    k_kv_append<D, BITS, F32><<<grid, threads, size_t(tile) * a.n_freq * sizeof(float2), st>>>(a, x, tile, norm_of(D));
+    return cudaGetLastError();
+  }
+};
+struct Read {
+  const KvArgs& a;
+  const KvDense& y;
+  cudaStream_t st;
+  template <int D, int BITS, bool F32>
+  cudaError_t go() {
+    const int tile = pick_tile(a.tokens);
+    const unsigned grid = unsigned((a.tokens + tile - 1) / tile);
+    k_kv_read<D, BITS, F32><<<grid, pick_threads(tile, a.hk, D / 32), 0, st>>>(a, y, tile, norm_of(D));
+    return cudaGetLastError();
+  }
+};
+
+}  // namespace
+
+cudaError_t launch_kv_append(const KvArgs& a, const KvDense& x, int dt, cudaStream_t st) {
+  return by_format(a, dt, Append{a, x, st});
+}
+cudaError_t launch_kv_read(const KvArgs& a, const KvDense& y, int dt, cudaStream_t st) {
+  return by_format(a, dt, Read{a, y, st});
+}
+
+}  // namespace hit

@@ -345,6 +345,112 @@ HIT_API int harp_blocks(const float* theta, const int8_t* theta_q, float theta_s
                         const float* mixer, const int8_t* signs, float* blocks, void* stream);
 
 /*
+ * Rotated key/value cache (not an operation of the pages: the online rotation
+ * of activations [HARP §4, inference side] applied to what attention caches,
+ * so that cached keys and values can be held in 4 or 8 bits).
+ *
+ * A rotation is an exact change of basis [HARP §5]: with R = H_d diag(s) /
+ * sqrt(d), (R q) . (R k) = q . k, and sum_j p_j v_j = R^-1 sum_j p_j (R v_j).
+ * The cache therefore holds R k and R v, whose outlier channels are spread
+ * over the head, quantized by symmetric absmax RTN with ONE scale per head
+ * vector (the group is the head):
+ *   u = R x;  a = max|u|;  s = a / qmax (qmax = 2^(bits-1) - 1);
+ *   q = clamp(rint(u / s), -qmax, qmax);  stored code q + 2^(bits-1),
+ * every step in IEEE fp32 and codes packed LSB first, as rht_quantize_pack's.
+ * a = 0 gives s = 0 and q = 0.  A vector with a NaN or an infinity in it is
+ * stored with s = NaN and q = 0: whatever attends to it is NaN.
+ *
+ * hit_kv describes the cache, the sequences of one call and the positions.
+ * All pointers are device pointers; the struct itself is read by the host
+ * during the call.
+ *  - k_codes, v_codes: uint8 [pages, kv_heads, page_size, head_dim*bits/8];
+ *    k_scales, v_scales: fp32 [pages, kv_heads, page_size]; all contiguous,
+ *    16-byte aligned bases.  head_dim 64, 128 or 256; bits 4 or 8; page_size a
+ *    power of two <= 65536.
+ *  - cu: int32 [seqs + 1], ascending; sequence s owns tokens cu[s] <= t <
+ *    cu[s+1] of the call (n_s of them, possibly none).  Tokens before cu[0]
+ *    and at or behind cu[seqs] belong to no sequence: their inputs are not
+ *    read and their outputs are left as they were.
+ *  - lens: int32 [seqs], the positions sequence s has, this call's tokens
+ *    included: token t has position lens[s] - n_s + (t - cu[s]).
+ *  - page_table: int32 [seqs, ld_table], max_pages of each row used; position
+ *    p lives in page page_table[s][p / page_size] at p % page_size.  Positions
+ *    below 0, behind max_pages pages or in a page outside [0, pages) do not
+ *    exist: nothing is written there, attention does not see them and reading
+ *    gives zeros (the kernels never access memory out of bounds).
+ *  - k_signs, v_signs: int8 [head_dim], the signs s of the two rotations, or
+ *    NULL for +1.
+ *  - inv_freq: fp32 [n_freq], rotary position frequencies applied to keys and
+ *    queries (not values) before the rotation, or NULL (n_freq 0).  The angle
+ *    of pair j is pos * inv_freq[j], evaluated in fp64 before its sine and
+ *    cosine are taken in fp32; (x, y) becomes (x cos - y sin, x sin + y cos).
+ *    Pairs are (j, j + n_freq), n_freq a multiple of 8, or with interleaved
+ *    != 0 (2j, 2j + 1), n_freq a multiple of 4; 2 n_freq <= head_dim, elements
+ *    from 2 n_freq on are not turned.
+ *  - positions: int32 [rope_axes, ld_positions], the rotary positions of the
+ *    call's tokens (column t), or NULL: each token's own position in its
+ *    sequence.  With several axes (time, height, width) rope_axis int8
+ *    [n_freq] names the axis of each pair; a pair whose axis is outside
+ *    [0, rope_axes) is not turned.  rope_axis may be NULL with one axis.
+ * Two tokens of one call must not share a slot (one of them would be stored).
+ *
+ * rht_kv_append: puts k and v [tokens, kv_heads, head_dim] (dtype, strides in
+ *   elements between tokens *_ts and heads *_hs, unit stride inside a head)
+ *   into the cache.
+ * rht_kv_attention: out[t, h] = R_v^-1 sum_j p_j (stored value j of key/value
+ *   head h / (heads / kv_heads)), p = softmax over the visible j of
+ *   sm_scale * (R_k rope(q[t, h])) . (stored key j).  A token at position p
+ *   sees j < lens[s], with causal != 0 only j <= p, and with window > 0 (causal
+ *   only) only j > p - window.  A token that sees nothing gets 0.  q, out:
+ *   [tokens, heads, head_dim], strided as k.  Arithmetic: scores as fp16 x
+ *   integer products with fp32 sums (q rounded once to fp16 behind a power of
+ *   two of its own row; the codes are exact), softmax in fp32, probabilities
+ *   (times the value's scale) rounded once to bf16, fp32 sums.  max_new: an
+ *   upper bound of n_s (any value >= 1 is right; a tight one saves a launch).
+ *   Needs rht_kv_workspace_bytes(heads, kv_heads, head_dim) bytes of 16-byte
+ *   aligned workspace, which calls that may run at the same time must not share.
+ * rht_kv_read: k, v [rows, kv_heads, head_dim] <- R^-1 of what the cache
+ *   stands for at the call's tokens (rows is the number of tokens; either
+ *   output may be NULL).  Keys come back with their rotary turn.
+ */
+typedef struct hit_kv {
+  uint8_t* k_codes;
+  float* k_scales;
+  uint8_t* v_codes;
+  float* v_scales;
+  const int32_t* page_table;
+  const int32_t* lens;
+  const int32_t* cu;
+  const int8_t* k_signs;
+  const int8_t* v_signs;
+  const float* inv_freq;
+  const int32_t* positions;
+  const int8_t* rope_axis;
+  int64_t pages;
+  int64_t page_size;
+  int64_t ld_table;
+  int64_t ld_positions;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t bits;
+  int32_t seqs;
+  int32_t max_pages;
+  int32_t n_freq;
+  int32_t rope_axes;
+  int32_t interleaved;
+} hit_kv;
+
+HIT_API int rht_kv_append(const hit_kv* kv, const void* k, const void* v, int64_t tokens, int64_t k_ts, int64_t k_hs,
+                          int64_t v_ts, int64_t v_hs, int dtype, void* stream);
+HIT_API size_t rht_kv_workspace_bytes(int heads, int kv_heads, int head_dim);
+HIT_API int rht_kv_attention(const hit_kv* kv, const void* q, void* out, int64_t tokens, int heads, int64_t q_ts,
+                             int64_t q_hs, int64_t o_ts, int64_t o_hs, int dtype_q, int dtype_out, float sm_scale,
+                             int causal, int64_t window, int64_t max_new, void* workspace, size_t workspace_bytes,
+                             void* stream);
+HIT_API int rht_kv_read(const hit_kv* kv, void* k, void* v, int64_t rows, int64_t k_ts, int64_t k_hs, int64_t v_ts,
+                        int64_t v_hs, int dtype, void* stream);
+
+/*
  * Fused RHT + group quantization without any allocation (no counterpart in
  * the pages; a deployment convenience).
  *
