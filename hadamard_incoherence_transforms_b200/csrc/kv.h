@@ -40,12 +40,15 @@ struct KvAttn {
   const void* q = nullptr;
   void* out = nullptr;
   int64_t q_ts = 0, q_hs = 0, o_ts = 0, o_hs = 0;
-  int heads = 0, q_f32 = 0, o_f32 = 0, causal = 1;
+  int heads = 0, group = 1;  // query heads; of one key/value head
+  int q_f32 = 0, o_f32 = 0, causal = 1;
+  int64_t rows_lo = 0, rows_hi = INT64_MAX;  // sequences with this many query rows (token * group) belong to the launch
   float scale = 1.0f;
   int64_t window = 0;
   int64_t max_new = 1;
   void* ws = nullptr;
 };
-cudaError_t launch_kv_attention(const KvArgs& a, const KvAttn& t, cudaStream_t st);
+size_t kv_few_bytes(int head_dim);  // workspace
+cudaError_t launch_kv_few(const KvArgs& a, const KvAttn& t, cudaStream_t st);
 
 }  // namespace hit

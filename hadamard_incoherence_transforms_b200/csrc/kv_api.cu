@@ -155,8 +155,8 @@ int rht_kv_read(const hit_kv* kv, void* k, void* v, int64_t rows, int64_t k_ts, 
 }
 
 size_t rht_kv_workspace_bytes(int heads, int kv_heads, int head_dim) {
-  (void)heads, (void)kv_heads, (void)head_dim;
-  return 0;
+  if (heads < 1 || kv_heads < 1 || (head_dim != 64 && head_dim != 128 && head_dim != 256)) return 0;
+  return hit::kv_few_bytes(head_dim);
 }
 
 int rht_kv_attention(const hit_kv* kv, const void* q, void* out, int64_t tokens, int heads, int64_t q_ts, int64_t q_hs,
@@ -193,14 +193,15 @@ int rht_kv_attention(const hit_kv* kv, const void* q, void* out, int64_t tokens,
   t.o_ts = o_ts;
   t.o_hs = o_hs;
   t.heads = heads;
+  t.group = heads / a.hk;
   t.q_f32 = dtype_q == HIT_F32;
   t.o_f32 = dtype_out == HIT_F32;
   t.causal = causal ? 1 : 0;
   t.scale = sm_scale;
   t.window = window;
-  t.max_new = max_new;
+  t.max_new = max_new < tokens ? max_new : tokens;
   t.ws = workspace;
-  return cuda_status(hit::launch_kv_attention(a, t, static_cast<cudaStream_t>(stream)), fn);
+  return cuda_status(hit::launch_kv_few(a, t, static_cast<cudaStream_t>(stream)), fn);
 }
 
 }  // extern "C"
