@@ -10,6 +10,7 @@
 #include "hit.h"
 #include "internal.h"
 #include "kernels.h"
+#include "kv.h"
 
 namespace {
 
@@ -313,6 +314,7 @@ int hit_wait_timeouts(unsigned long long* count, int reset) {
   if (e == cudaSuccess) e = hit::wait_timeouts_mixed(&n, reset != 0);
   if (e == cudaSuccess) e = hit::wait_timeouts_tc(&n, reset != 0);
   if (e == cudaSuccess) e = hit::wait_timeouts_strided(&n, reset != 0);
+  if (e == cudaSuccess) e = hit::wait_timeouts_kv(&n, reset != 0);
   if (e != cudaSuccess) return cuda_status(e, "hit_wait_timeouts: counter read");
   if (count != nullptr) *count += n;
   if (n != 0)

@@ -74,6 +74,20 @@ __device__ __forceinline__ float2 kv_angle(const KvArgs& a, int64_t t, int64_t p
   return make_float2(c, s);
 }
 
+// The same for queries: sine and cosine to 2^-21 by the hardware's functions, as
+// a query is rounded to 2^-11 after its turn anyway.
+__device__ __forceinline__ float2 kv_angle_fast(const KvArgs& a, int64_t t, int64_t pos, int j) {
+  int64_t p = pos;
+  if (a.positions != nullptr) {
+    const int ax = a.rope_axis != nullptr ? __ldg(a.rope_axis + j) : 0;
+    if (ax < 0 || ax >= a.rope_axes) return make_float2(1.0f, 0.0f);
+    p = __ldg(a.positions + int64_t(ax) * a.ld_pos + t);
+  }
+  const double turns = double(int(p)) * double(__ldg(a.inv_freq + j)) * 0.15915494309189533577;
+  const float x = float(turns - rint(turns)) * 6.2831853071795865f;
+  return make_float2(__cosf(x), __sinf(x));
+}
+
 // ---------------------------------------------------------------------------
 // A head vector of D elements on LPV = D / 32 neighbouring lanes: lane l of
 // them holds the four 8-element chunks l, l + LPV, l + 2 LPV, l + 3 LPV
@@ -108,6 +122,26 @@ __device__ __forceinline__ void kv_signs(float (&x)[32], const int8_t* __restric
       x[8 * c + e] = __uint_as_float(__float_as_uint(x[8 * c + e]) ^ ((b << 24) & 0x80000000u));
     }
   }
+}
+
+// Unnormalised rotated query x to base-2 scores, and the power of two `up` of
+// the row's largest element with `down` = 1 / up: x * down is in [-2, 2), where
+// fp16 keeps it to half a step of 2^-10 of its largest element or better.
+template <int D>
+__device__ __forceinline__ void kv_query_scale(float (&x)[32], float scale, float& up, float& down) {
+  const float f = (D == 64 ? 0.125f : D == 256 ? 0.0625f : 0.08838834764831845f) * 1.4426950408889634f * scale;
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    x[i] *= f;
+    m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
+  }
+#pragma unroll
+  for (int b = 0; b < KvLanes<D>::LOG; ++b) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1 << b));
+  const uint32_t ex = max(1u, m >> 23);
+  const bool odd = ex == 255;  // an infinity or a NaN: left to spread
+  up = odd ? 1.0f : __uint_as_float(ex << 23);
+  down = odd ? 1.0f : __uint_as_float(ex == 254 ? 0x00400000u : (254 - ex) << 23);
 }
 
 // Eight consecutive elements as fp32.
@@ -166,6 +200,51 @@ __device__ __forceinline__ void kv_rope(float (&x)[32], const void* p, int64_t a
       for (int e = 0; e < 8; ++e) {
         const float2 t = cs[j0 + e];
         v[e] = low ? v[e] * t.x - o[e] * t.y : o[e] * t.y + v[e] * t.x;
+      }
+    }
+  }
+}
+
+// The same turn with the angles found on the way (positions and queries of
+// long calls, where a table of them would not fit).
+template <int D, bool F32>
+__device__ __forceinline__ void kv_rope_direct(float (&x)[32], const void* src, int64_t at, const KvArgs& a, int64_t t,
+                                               int64_t pos, int l) {
+  constexpr int LPV = KvLanes<D>::LPV;
+  if (a.interleaved) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int i0 = 8 * (c * LPV + l);
+      if (i0 >= 2 * a.n_freq) continue;
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        const float2 cs = kv_angle_fast(a, t, pos, (i0 + e) / 2);
+        const float u = x[8 * c + e], w = x[8 * c + e + 1];
+        x[8 * c + e] = u * cs.x - w * cs.y;
+        x[8 * c + e + 1] = u * cs.y + w * cs.x;
+      }
+    }
+  } else if (2 * a.n_freq == D) {  // both chunks of a pair are the lane's own
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float2 cs = kv_angle_fast(a, t, pos, 8 * ((i / 8) * LPV + l) + i % 8);
+      const float u = x[i], w = x[i + 16];
+      x[i] = u * cs.x - w * cs.y;
+      x[i + 16] = u * cs.y + w * cs.x;
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int i0 = 8 * (c * LPV + l);
+      if (i0 >= 2 * a.n_freq) continue;
+      const bool low = i0 < a.n_freq;
+      float o[8];
+      kv_load8<F32>(src, at + (low ? i0 + a.n_freq : i0 - a.n_freq), o);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float2 cs = kv_angle_fast(a, t, pos, (low ? i0 : i0 - a.n_freq) + e);
+        float& v = x[8 * c + e];
+        v = low ? v * cs.x - o[e] * cs.y : o[e] * cs.y + v * cs.x;
       }
     }
   }

@@ -1,5 +1,6 @@
 // C ABI of the rotated key/value cache (declared in include/hit.h): host-side
 // argument checks and dispatch.  Every check runs before the first CUDA call.
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -28,6 +29,7 @@ int cuda_status(cudaError_t e, const char* what) {
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 constexpr int64_t kMaxTokens = int64_t(1) << 31;
+constexpr int64_t kFewRows = 16;
 
 // Checks what the three calls share and fills `a`.  `rope`: whether the call
 // uses the rotary fields.
@@ -156,7 +158,7 @@ int rht_kv_read(const hit_kv* kv, void* k, void* v, int64_t rows, int64_t k_ts, 
 
 size_t rht_kv_workspace_bytes(int heads, int kv_heads, int head_dim) {
   if (heads < 1 || kv_heads < 1 || (head_dim != 64 && head_dim != 128 && head_dim != 256)) return 0;
-  return hit::kv_few_bytes(head_dim);
+  return std::max(hit::kv_few_bytes(head_dim), hit::kv_prompt_bytes(head_dim));
 }
 
 int rht_kv_attention(const hit_kv* kv, const void* q, void* out, int64_t tokens, int heads, int64_t q_ts, int64_t q_hs,
@@ -201,7 +203,17 @@ int rht_kv_attention(const hit_kv* kv, const void* q, void* out, int64_t tokens,
   t.window = window;
   t.max_new = max_new < tokens ? max_new : tokens;
   t.ws = workspace;
-  return cuda_status(hit::launch_kv_few(a, t, static_cast<cudaStream_t>(stream)), fn);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // Sequences with up to kFewRows query rows for a key/value head go to the kernel
+  // that streams the codes once for 16 rows, the others to the one that works
+  // on 256 rows at a time; each launch leaves the other's sequences alone, so
+  // that max_new decides only whether the second launch is needed.
+  if (a.head_dim == 256 || t.max_new * t.group <= kFewRows) return cuda_status(hit::launch_kv_few(a, t, st), fn);
+  hit::KvAttn few = t;
+  few.rows_hi = few.max_new = kFewRows;
+  t.rows_lo = kFewRows + 1;
+  r = cuda_status(hit::launch_kv_few(a, few, st), fn);
+  return r ? r : cuda_status(hit::launch_kv_prompt(a, t, st), fn);
 }
 
 }  // extern "C"

@@ -1,0 +1,63 @@
+// Stored codes to matrix operands, in registers and without an error: fp16 for
+// keys, bf16 for values (the other operand of a value is a probability times a
+// scale, which spans more than fp16's range).
+#pragma once
+#include <stdint.h>
+
+namespace hit {
+
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t m, uint32_t o) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(m), "r"(o));
+  return r;
+}
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t badd2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t bfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+
+// Eight 4-bit codes -> (0, 4), (1, 5), (2, 6), (3, 7) as fp16 pairs: 0x6400 | u
+// is 1024 + u, and 1024 + 16 u for the upper nibble of a byte.
+__device__ __forceinline__ void half_of4(uint32_t w, uint32_t (&h)[4]) {
+  const uint32_t v = w >> 8;
+  h[0] = hadd2(and_or(w, 0x000f000fu, 0x64006400u), 0xe408e408u);               // - 1032
+  h[1] = hfma2(and_or(w, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd480d480u);  // / 16 - 72
+  h[2] = hadd2(and_or(v, 0x000f000fu, 0x64006400u), 0xe408e408u);
+  h[3] = hfma2(and_or(v, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd480d480u);
+}
+// Four 8-bit codes -> (0, 1), (2, 3) as fp16 pairs.
+__device__ __forceinline__ void half_of8(uint32_t w, uint32_t& a, uint32_t& b) {
+  a = hadd2(__byte_perm(w, 0x64646464u, 0x4140), 0xe480e480u);  // 1024 + u - 1152
+  b = hadd2(__byte_perm(w, 0x64646464u, 0x4342), 0xe480e480u);
+}
+// x: two runs of 16 bits of codes.  4-bit codes -> (code n of the low run, code n
+// of the high one), n = 0 .. 3, as bf16 pairs.
+__device__ __forceinline__ void bf_of4(uint32_t x, uint32_t (&b)[4]) {
+#pragma unroll
+  for (int n = 0; n < 4; ++n) b[n] = badd2(and_or(x >> (4 * n), 0x000f000fu, 0x43004300u), 0xc308c308u);  // 128 + u - 136
+}
+// 8-bit codes, n = 0, 1: 16 h + l - 128 from its nibbles, every step exact.
+__device__ __forceinline__ void bf_of8(uint32_t x, uint32_t& b0, uint32_t& b1) {
+  const uint32_t l0 = and_or(x, 0x000f000fu, 0x43004300u), h0 = and_or(x >> 4, 0x000f000fu, 0x43004300u);
+  const uint32_t l1 = and_or(x >> 8, 0x000f000fu, 0x43004300u), h1 = and_or(x >> 12, 0x000f000fu, 0x43004300u);
+  b0 = badd2(bfma2(h0, 0x41804180u, 0xc510c510u), l0);  // (128 + h) * 16 - 2304 + 128 + l
+  b1 = badd2(bfma2(h1, 0x41804180u, 0xc510c510u), l1);
+}
+
+}  // namespace hit

@@ -17,6 +17,7 @@
 // O^T += V^T P^T takes P^T from the score accumulators with one 8x8 transpose
 // per 8 positions.  Scales never touch the codes: the key's multiplies its
 // score, the value's its probability.
+#include "kv_codes.cuh"
 #include "kv_split.cuh"
 
 #include <cuda_fp16.h>
@@ -42,60 +43,6 @@ struct Few {
   static constexpr int STAGE = TK * (2 * VB + 8) + 16;
   static constexpr int KS = D / 16;
 };
-
-__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t m, uint32_t o) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(m), "r"(o));
-  return r;
-}
-__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t r;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  return r;
-}
-__device__ __forceinline__ uint32_t badd2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t bfma2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t r;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  return r;
-}
-
-// Eight 4-bit codes -> (0, 4), (1, 5), (2, 6), (3, 7) as fp16 pairs: 0x6400 | u
-// is 1024 + u, and 1024 + 16 u for the upper nibble of a byte.
-__device__ __forceinline__ void half_of4(uint32_t w, uint32_t (&h)[4]) {
-  const uint32_t v = w >> 8;
-  h[0] = hadd2(and_or(w, 0x000f000fu, 0x64006400u), 0xe408e408u);               // - 1032
-  h[1] = hfma2(and_or(w, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd480d480u);  // / 16 - 72
-  h[2] = hadd2(and_or(v, 0x000f000fu, 0x64006400u), 0xe408e408u);
-  h[3] = hfma2(and_or(v, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd480d480u);
-}
-// Four 8-bit codes -> (0, 1), (2, 3) as fp16 pairs.
-__device__ __forceinline__ void half_of8(uint32_t w, uint32_t& a, uint32_t& b) {
-  a = hadd2(__byte_perm(w, 0x64646464u, 0x4140), 0xe480e480u);  // 1024 + u - 1152
-  b = hadd2(__byte_perm(w, 0x64646464u, 0x4342), 0xe480e480u);
-}
-// x: 16 bits of codes of one position below 16 bits of another.  4-bit codes
-// -> (code n of the one, code n of the other), n = 0 .. 3, as bf16 pairs.
-__device__ __forceinline__ void bf_of4(uint32_t x, uint32_t (&b)[4]) {
-#pragma unroll
-  for (int n = 0; n < 4; ++n) b[n] = badd2(and_or(x >> (4 * n), 0x000f000fu, 0x43004300u), 0xc308c308u);  // 128 + u - 136
-}
-// 8-bit codes, n = 0, 1: 16 h + l - 128 from its nibbles, every step exact.
-__device__ __forceinline__ void bf_of8(uint32_t x, uint32_t& b0, uint32_t& b1) {
-  const uint32_t l0 = and_or(x, 0x000f000fu, 0x43004300u), h0 = and_or(x >> 4, 0x000f000fu, 0x43004300u);
-  const uint32_t l1 = and_or(x >> 8, 0x000f000fu, 0x43004300u), h1 = and_or(x >> 12, 0x000f000fu, 0x43004300u);
-  b0 = badd2(bfma2(h0, 0x41804180u, 0xc510c510u), l0);  // (128 + h) * 16 - 2304 + 128 + l
-  b1 = badd2(bfma2(h1, 0x41804180u, 0xc510c510u), l1);
-}
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -241,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
       static_assert(sizeof(float2) * ROWS * (D / 2) + 2 * ROWS * QP + 4 * ROWS <= 2 * kWarps * F::STAGE, "scratch");
       for (int i = threadIdx.x; i < (i1 - i0 + 1) * a.n_freq; i += kThreads) {
         const int j = i / a.n_freq;
-        cs[i] = kv_angle(a, q.t0 + i0 + j, q.pos0 + i0 + j, i - j * a.n_freq);
+        cs[i] = kv_angle_fast(a, q.t0 + i0 + j, q.pos0 + i0 + j, i - j * a.n_freq);
       }
       __syncthreads();
       constexpr int LPV = KvLanes<D>::LPV;
@@ -266,20 +213,8 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
           kv_signs<D>(x, a.k_signs, l);
         }
         kv_hadamard<D>(x, l);
-        const float f = (D == 64 ? 0.125f : D == 256 ? 0.0625f : 0.08838834764831845f) * 1.4426950408889634f * t.scale;
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          x[i] *= f;
-          m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
-        }
-#pragma unroll
-        for (int b = 0; b < KvLanes<D>::LOG; ++b) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1 << b));
-        // 2^e and 2^-e with e the exponent of the row's largest element
-        const uint32_t ex = max(1u, m >> 23);
-        const bool odd = ex == 255;  // an infinity or a NaN: left to spread
-        const float up = odd ? 1.0f : __uint_as_float(ex << 23);
-        const float down = odd ? 1.0f : __uint_as_float(ex == 254 ? 0x00400000u : (254 - ex) << 23);
+        float up, down;
+        kv_query_scale<D>(x, t.scale, up, down);
         if (r < ROWS) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
