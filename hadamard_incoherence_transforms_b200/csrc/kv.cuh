@@ -57,34 +57,40 @@ __device__ __forceinline__ KvToken kv_token(const KvArgs& a, int64_t t, int lane
   return k;
 }
 
-// Cosine and sine of pair j of token t at sequence position pos.  The product
-// is formed and reduced to a fraction of a turn in fp64 (a position of 10^6
-// would leave fp32 no correct digits), the functions are taken in fp32.
-__device__ __forceinline__ float2 kv_angle(const KvArgs& a, int64_t t, int64_t pos, int j) {
-  int64_t p = pos;
-  if (a.positions != nullptr) {
-    const int ax = a.rope_axis != nullptr ? __ldg(a.rope_axis + j) : 0;
-    if (ax < 0 || ax >= a.rope_axes) return make_float2(1.0f, 0.0f);
-    p = __ldg(a.positions + int64_t(ax) * a.ld_pos + t);
-  }
-  const double turns = double(p) * double(__ldg(a.inv_freq + j)) * 0.15915494309189533577;
-  const float frac = float(2.0 * (turns - rint(turns)));
+// Rotary angles.  A frequency is held as the fraction of a turn that one
+// position makes, in units of 2^-64: a position times it, modulo 2^64, is the
+// angle's fraction of a turn, exactly, in one integer product (in fp32 a
+// position of 10^6 would leave no correct digits).  kv_turn gives the units of
+// a frequency, found in fp64 once per CTA and pair.
+__device__ __forceinline__ uint64_t kv_turn(const KvArgs& a, int j) {
+  const double f = double(__ldg(a.inv_freq + j)) * 0.15915494309189533577;
+  return __double2ull_rz((f - floor(f)) * 18446744073709551616.0);
+}
+// The table of all pairs; followed by a barrier of the caller's.
+__device__ __forceinline__ void kv_turns(const KvArgs& a, uint64_t* turns, int thread, int threads) {
+  for (int j = thread; j < a.n_freq; j += threads) turns[j] = kv_turn(a, j);
+}
+// Position that pair j of token t (at sequence position pos) turns by.
+__device__ __forceinline__ int kv_turn_pos(const KvArgs& a, int64_t t, int pos, int j) {
+  if (a.positions == nullptr) return pos;
+  const int ax = a.rope_axis != nullptr ? __ldg(a.rope_axis + j) : 0;
+  // a pair without an axis is not turned
+  return ax < 0 || ax >= a.rope_axes ? 0 : __ldg(a.positions + int64_t(ax) * a.ld_pos + t);
+}
+// Twice the angle's fraction of a turn, in [-1, 1].
+__device__ __forceinline__ float kv_halfturns(int pos, uint64_t turn) {
+  return float(int(uint64_t(int64_t(pos) * int64_t(turn)) >> 32)) * 4.656612873077393e-10f;
+}
+// (cos, sin) to fp32's precision, for keys.
+__device__ __forceinline__ float2 kv_angle(const KvArgs& a, const uint64_t* turns, int64_t t, int pos, int j) {
   float s, c;
-  sincospif(frac, &s, &c);
+  sincospif(kv_halfturns(kv_turn_pos(a, t, pos, j), turns[j]), &s, &c);
   return make_float2(c, s);
 }
-
-// The same for queries: sine and cosine to 2^-21 by the hardware's functions, as
-// a query is rounded to 2^-11 after its turn anyway.
-__device__ __forceinline__ float2 kv_angle_fast(const KvArgs& a, int64_t t, int64_t pos, int j) {
-  int64_t p = pos;
-  if (a.positions != nullptr) {
-    const int ax = a.rope_axis != nullptr ? __ldg(a.rope_axis + j) : 0;
-    if (ax < 0 || ax >= a.rope_axes) return make_float2(1.0f, 0.0f);
-    p = __ldg(a.positions + int64_t(ax) * a.ld_pos + t);
-  }
-  const double turns = double(int(p)) * double(__ldg(a.inv_freq + j)) * 0.15915494309189533577;
-  const float x = float(turns - rint(turns)) * 6.2831853071795865f;
+// The same to 2^-21 by the hardware's functions, for queries, which are rounded
+// to 2^-11 after their turn.
+__device__ __forceinline__ float2 kv_angle_fast(const KvArgs& a, const uint64_t* turns, int64_t t, int pos, int j) {
+  const float x = kv_halfturns(kv_turn_pos(a, t, pos, j), turns[j]) * 3.14159265358979f;
   return make_float2(__cosf(x), __sinf(x));
 }
 
@@ -208,8 +214,8 @@ __device__ __forceinline__ void kv_rope(float (&x)[32], const void* p, int64_t a
 // The same turn with the angles found on the way (positions and queries of
 // long calls, where a table of them would not fit).
 template <int D, bool F32>
-__device__ __forceinline__ void kv_rope_direct(float (&x)[32], const void* src, int64_t at, const KvArgs& a, int64_t t,
-                                               int64_t pos, int l) {
+__device__ __forceinline__ void kv_rope_direct(float (&x)[32], const void* src, int64_t at, const KvArgs& a,
+                                               const uint64_t* turns, int64_t t, int pos, int l) {
   constexpr int LPV = KvLanes<D>::LPV;
   if (a.interleaved) {
 #pragma unroll
@@ -218,7 +224,7 @@ __device__ __forceinline__ void kv_rope_direct(float (&x)[32], const void* src, 
       if (i0 >= 2 * a.n_freq) continue;
 #pragma unroll
       for (int e = 0; e < 8; e += 2) {
-        const float2 cs = kv_angle_fast(a, t, pos, (i0 + e) / 2);
+        const float2 cs = kv_angle_fast(a, turns, t, pos, (i0 + e) / 2);
         const float u = x[8 * c + e], w = x[8 * c + e + 1];
         x[8 * c + e] = u * cs.x - w * cs.y;
         x[8 * c + e + 1] = u * cs.y + w * cs.x;
@@ -227,7 +233,7 @@ __device__ __forceinline__ void kv_rope_direct(float (&x)[32], const void* src, 
   } else if (2 * a.n_freq == D) {  // both chunks of a pair are the lane's own
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const float2 cs = kv_angle_fast(a, t, pos, 8 * ((i / 8) * LPV + l) + i % 8);
+      const float2 cs = kv_angle_fast(a, turns, t, pos, 8 * ((i / 8) * LPV + l) + i % 8);
       const float u = x[i], w = x[i + 16];
       x[i] = u * cs.x - w * cs.y;
       x[i + 16] = u * cs.y + w * cs.x;
@@ -242,7 +248,7 @@ __device__ __forceinline__ void kv_rope_direct(float (&x)[32], const void* src, 
       kv_load8<F32>(src, at + (low ? i0 + a.n_freq : i0 - a.n_freq), o);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float2 cs = kv_angle_fast(a, t, pos, (low ? i0 : i0 - a.n_freq) + e);
+        const float2 cs = kv_angle_fast(a, turns, t, pos, (low ? i0 : i0 - a.n_freq) + e);
         float& v = x[8 * c + e];
         v = low ? v * cs.x - o[e] * cs.y : o[e] * cs.y + v * cs.x;
       }

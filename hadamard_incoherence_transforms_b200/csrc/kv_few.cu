@@ -112,6 +112,8 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
   constexpr int OM = D / 16;   // 16-element tiles of the output's head dimension
   constexpr int QP = D + 8;    // padded row of the query in shared memory
   extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ uint64_t turns[D / 2];
+  kv_turns(a, turns, threadIdx.x, kThreads);  // kv_plan's barriers follow
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r8 = lane >> 2, c4 = lane & 3;
   const KvPlan plan = kv_plan<ROWS, TK, kThreads>(a, t, kWarps);
   const KvWork work = kv_work_of<D, ROWS>(t.ws, gridDim.x);
@@ -188,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
       static_assert(sizeof(float2) * ROWS * (D / 2) + 2 * ROWS * QP + 4 * ROWS <= 2 * kWarps * F::STAGE, "scratch");
       for (int i = threadIdx.x; i < (i1 - i0 + 1) * a.n_freq; i += kThreads) {
         const int j = i / a.n_freq;
-        cs[i] = kv_angle_fast(a, q.t0 + i0 + j, q.pos0 + i0 + j, i - j * a.n_freq);
+        cs[i] = kv_angle_fast(a, turns, q.t0 + i0 + j, int(q.pos0) + i0 + j, i - j * a.n_freq);
       }
       __syncthreads();
       constexpr int LPV = KvLanes<D>::LPV;

@@ -270,19 +270,25 @@ __host__ __device__ constexpr uint32_t instr_desc(bool bf16, int n, bool b_mn_ma
   return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (uint32_t(b_mn_major) << 16) | (uint32_t(n >> 3) << 17) |
          (uint32_t(128 >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool add) {
+// Shared-memory descriptors as their two words.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t id, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(uint32_t(add))
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(id), "r"(uint32_t(add))
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi, uint32_t id, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"(uint32_t(add))
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(hi), "r"(id), "r"(uint32_t(add))
       : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 __device__ __forceinline__ void commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
@@ -297,7 +303,28 @@ __device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t (&r)[32]) {
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(at));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+// Waits for the thread's loads; v: what must not be used before.
+__device__ __forceinline__ void tmem_load_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])::"memory");
+}
+__device__ __forceinline__ void tmem_load32_now(uint32_t at, uint32_t (&r)[32]) {
+  tmem_load32(at, r);
+  tmem_load_wait(r);
+}
+__device__ __forceinline__ void tmem_load16_now(uint32_t at, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at)
+      : "memory");
 }
 __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&r)[16]) {
   asm volatile(
@@ -310,8 +337,15 @@ __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&r)[16
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// Loads that stay where they are written.
+__device__ __forceinline__ void load16(uint4& x, const void* p) {
+  asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(p));
+}
+__device__ __forceinline__ void load4(float& x, const float* p) {
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(x) : "l"(p));
+}
 // Registers of a group of four warps (all four run it).  The kernel starts with
-// 128 a thread; 2 x 160 + 128 + 64 are the same 512.
+// 128 a thread; 2 x 176 + 112 + 48 are the same 512.
 template <int N>
 __device__ __forceinline__ void regs_more() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -320,11 +354,121 @@ template <int N>
 __device__ __forceinline__ void regs_less() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
+// {a0, a1} += {b0, b1}
+__device__ __forceinline__ void add_x2(float& a0, float& a1, float b0, float b1) {
+  unsigned long long A = pk2(a0, a1), B = pk2(b0, b1), R;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(R) : "l"(A), "l"(B));
+  upk2(R, a0, a1);
+}
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+
+// One row's softmax of a unit: its 128 scores in tensor memory become
+// probabilities times value scales (bf16, in the same place).  m: the maximum
+// they are relative to, l: the sum of probabilities, fix: what sums from before
+// have to be multiplied with.  FULL: every column is seen.
+//
+// 32 columns at a time, against the maximum so far; where some row's scores
+// exceed it by more than 2^kGrow (or it has none yet) the warp takes the larger
+// one for the rows that need it and brings the columns already done (and, through
+// `fix`, l and O) to it.  The usual unit is one pass over its scores.  The loop
+// is not unrolled: the roles share the instruction cache.
+template <bool FULL>
+struct UnitSoftmax {
+  uint32_t s_at;
+  const float4 *ks, *vs;
+  uint4 there;
+  int c_lo, c_hi;
+  float qe;
+
+  __device__ __forceinline__ uint32_t seen(int c) const {  // of columns 32 c .. 32 c + 31
+    const uint32_t e = c == 0 ? there.x : c == 1 ? there.y : c == 2 ? there.z : there.w;
+    const int x0 = max(0, min(32, c_lo - 32 * c)), x1 = max(0, min(32, c_hi - 32 * c));
+    const uint32_t below = x1 == 32 ? ~0u : (1u << x1) - 1, under = x0 == 32 ? ~0u : (1u << x0) - 1;
+    return e & below & ~under;
+  }
+  // Base-2 scores of 32 columns below `base`, and the largest.
+  __device__ __forceinline__ float scores(const uint32_t (&v)[32], int c, float base, float (&x)[32]) const {
+    const uint32_t see = FULL ? ~0u : seen(c);
+    float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+      const float4 k = ks[8 * c + i / 4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[i + e] = __uint_as_float(v[i + e]);
+      mul_x2(x[i], x[i + 1], k.x, k.y);
+      mul_x2(x[i + 2], x[i + 3], k.z, k.w);
+      fma_x2(x[i], x[i + 1], qe, qe, base, base, x[i], x[i + 1]);
+      fma_x2(x[i + 2], x[i + 3], qe, qe, base, base, x[i + 2], x[i + 3]);
+      if constexpr (!FULL) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[i + e] = (see >> (i + e)) & 1 ? x[i + e] : -INFINITY;
+      }
+      t0 = fmaxf(t0, fmaxf(x[i], x[i + 1]));
+      t1 = fmaxf(t1, fmaxf(x[i + 2], x[i + 3]));
+    }
+    return fmaxf(t0, t1);
+  }
+  __device__ __forceinline__ void run(float& m, float& l, float& fix) const {
+    float base = m == -INFINITY ? 0.0f : -m;
+    float l0 = l, l1 = 0.0f;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      uint32_t v[32];
+      tmem_load32_now(s_at + 32 * c, v);
+      float x[32];
+      const float top = scores(v, c, base, x);
+      const bool grow = top > kGrow || (m == -INFINITY && top > m);
+      if (__any_sync(0xffffffffu, grow)) {
+        const float f = grow ? (m == -INFINITY ? 0.0f : ex2(-top)) : 1.0f;
+        if (grow) {
+          base -= top;
+          m = -base;
+        }
+        fix *= f;
+        l0 *= f;
+        l1 *= f;
+        scores(v, c, base, x);
+        tmem_store_wait();
+#pragma unroll 1
+        for (int k = 0; k < c; ++k) {
+          uint32_t p[16];
+          tmem_load16_now(s_at + 16 * k, p);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float u, w;
+            bf16x2_to_f32(p[i], u, w);
+            p[i] = f32_to_bf16x2(u * f, w * f);
+          }
+          tmem_store16(s_at + 16 * k, p);
+        }
+      }
+      uint32_t p[16];
+      const uint32_t see = FULL ? ~0u : seen(c);
+#pragma unroll
+      for (int i = 0; i < 32; i += 4) {
+        const float4 z = vs[8 * c + i / 4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[i + e] = ex2(x[i + e]);
+        add_x2(l0, l1, x[i], x[i + 1]);
+        add_x2(l0, l1, x[i + 2], x[i + 3]);
+        mul_x2(x[i], x[i + 1], z.x, z.y);
+        mul_x2(x[i + 2], x[i + 3], z.z, z.w);
+        if constexpr (!FULL) {  // the scale of a position that is not seen may be anything
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[i + e] = (see >> (i + e)) & 1 ? x[i + e] : 0.0f;
+        }
+        p[i / 2] = f32_to_bf16x2(x[i], x[i + 1]);
+        p[i / 2 + 1] = f32_to_bf16x2(x[i + 2], x[i + 3]);
+      }
+      tmem_store16(s_at + 16 * c, p);
+    }
+    l = l0 + l1;
+  }
+};
 
 // Element of the head that column c of an 8-column chunk of K, Q and V holds:
 // the order in which the codes fall out of a word.
@@ -365,6 +509,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  __shared__ uint64_t turns[D / 2];
+  __shared__ uint32_t k_neg[D / 32], v_neg[D / 32];  // a bit for each element whose sign is flipped
+  kv_turns(a, turns, threadIdx.x, kThreads);
+  if (warp >= 4 && warp < 4 + D / 32) {
+    const int i = 32 * (warp - 4) + lane;
+    const uint32_t kb = __ballot_sync(0xffffffffu, a.k_signs != nullptr && __ldg(a.k_signs + i) < 0);
+    const uint32_t vb = __ballot_sync(0xffffffffu, a.v_signs != nullptr && __ldg(a.v_signs + i) < 0);
+    if (lane == 0) k_neg[warp - 4] = kb, v_neg[warp - 4] = vb;
+  }
   if (warp == 0) plan_warp(a, t, bars, lane);
   fence_before();
   __syncthreads();
@@ -377,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
 
   Walk w;
   if (warp < 8) {
-    regs_more<160>();
+    regs_more<176>();
     w.start(bars);
     // ---------------- softmax of half `hf`, a thread a row ----------------
     const int hf = warp >> 2, r = threadIdx.x & 127;
@@ -403,6 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
         // the half's queries: turned, rotated, scaled into base-2 scores, brought to [-2, 2)
         constexpr int LPV = KvLanes<D>::LPV;
         const int ln = r % LPV;
+#pragma unroll 1
         for (int q0 = 0; q0 < 128; q0 += 128 / LPV) {
           const int qr = q0 + r / LPV;
           float x[32];
@@ -414,13 +568,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
             if (t.q_f32) {
 #pragma unroll
               for (int c = 0; c < 4; ++c) kv_load8<true>(t.q, src + 8 * (c * LPV + ln), x + 8 * c);
-              if (a.n_freq > 0) kv_rope_direct<D, true>(x, t.q, src, a, g.q.t0 + tk, g.q.pos0 + tk, ln);
+              if (a.n_freq > 0) kv_rope_direct<D, true>(x, t.q, src, a, turns, g.q.t0 + tk, int(g.q.pos0) + tk, ln);
             } else {
 #pragma unroll
               for (int c = 0; c < 4; ++c) kv_load8<false>(t.q, src + 8 * (c * LPV + ln), x + 8 * c);
-              if (a.n_freq > 0) kv_rope_direct<D, false>(x, t.q, src, a, g.q.t0 + tk, g.q.pos0 + tk, ln);
+              if (a.n_freq > 0) kv_rope_direct<D, false>(x, t.q, src, a, turns, g.q.t0 + tk, int(g.q.pos0) + tk, ln);
             }
-            kv_signs<D>(x, a.k_signs, ln);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int ch = c * LPV + ln;
+              const uint32_t neg = k_neg[ch >> 2] >> (8 * (ch & 3));
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                x[8 * c + e] = __uint_as_float(__float_as_uint(x[8 * c + e]) ^ ((neg << (31 - e)) & 0x80000000u));
+            }
           }
           kv_hadamard<D>(x, ln);
           float up, down;
@@ -464,72 +625,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
           // columns [c_lo, c_hi) are this row's
           const int c_lo = int(max(int64_t(0), min(int64_t(128), lo - p0)));
           const int c_hi = int(max(int64_t(0), min(int64_t(128), hi - p0)));
-          auto seen = [&](int c) {  // of columns 32 c .. 32 c + 31
-            const uint32_t e = c == 0 ? there.x : c == 1 ? there.y : c == 2 ? there.z : there.w;
-            const int x0 = max(0, min(32, c_lo - 32 * c)), x1 = max(0, min(32, c_hi - 32 * c));
-            const uint32_t below = x1 == 32 ? ~0u : (1u << x1) - 1, under = x0 == 32 ? ~0u : (1u << x0) - 1;
-            return e & below & ~under;
-          };
-          float top = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[32];
-            tmem_load32(s_at + 32 * c, v);
-            const uint32_t see = full ? ~0u : seen(c);
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 k = ks[8 * c + i / 4];
-              float x0 = __uint_as_float(v[i]), x1 = __uint_as_float(v[i + 1]), x2 = __uint_as_float(v[i + 2]),
-                    x3 = __uint_as_float(v[i + 3]);
-              mul_x2(x0, x1, k.x, k.y);
-              mul_x2(x2, x3, k.z, k.w);
-              if (!full) {
-                x0 = (see >> i) & 1 ? x0 : -INFINITY;
-                x1 = (see >> (i + 1)) & 1 ? x1 : -INFINITY;
-                x2 = (see >> (i + 2)) & 1 ? x2 : -INFINITY;
-                x3 = (see >> (i + 3)) & 1 ? x3 : -INFINITY;
-              }
-              top = fmaxf(fmaxf(top, fmaxf(x0, x1)), fmaxf(x2, x3));
-            }
-          }
-          top *= qe;
-          // a new reference when the maximum has grown too far (or is the first)
           float fix = 1.0f;
-          if (top > m + kGrow || (m == -INFINITY && top > m)) {
-            fix = ex2(m - top);
-            m = top;
-          }
-          const float base = m == -INFINITY ? 0.0f : -m;
-          float l0 = l * fix, l1 = 0.0f;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[32], p[16];
-            tmem_load32(s_at + 32 * c, v);
-            const uint32_t see = full ? ~0u : seen(c);
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float4 k = ks[8 * c + i / 4], z = vs[8 * c + i / 4];
-              float x0 = __uint_as_float(v[i]), x1 = __uint_as_float(v[i + 1]);
-              mul_x2(x0, x1, i & 2 ? k.z : k.x, i & 2 ? k.w : k.y);
-              fma_x2(x0, x1, qe, qe, base, base, x0, x1);
-              x0 = ex2(x0);
-              x1 = ex2(x1);
-              if (!full) {
-                x0 = (see >> i) & 1 ? x0 : 0.0f;
-                x1 = (see >> (i + 1)) & 1 ? x1 : 0.0f;
-              }
-              l0 += x0;
-              l1 += x1;
-              mul_x2(x0, x1, i & 2 ? z.z : z.x, i & 2 ? z.w : z.y);
-              if (!full) {
-                x0 = (see >> i) & 1 ? x0 : 0.0f;
-                x1 = (see >> (i + 1)) & 1 ? x1 : 0.0f;
-              }
-              p[i / 2] = f32_to_bf16x2(x0, x1);
-            }
-            tmem_store16(s_at + 16 * c, p);
-          }
-          l = l0 + l1;
+          if (full) UnitSoftmax<true>{s_at, ks, vs, there, 0, kKeys, qe}.run(m, l, fix);
+          else UnitSoftmax<false>{s_at, ks, vs, there, c_lo, c_hi, qe}.run(m, l, fix);
           if (j > f.js && __any_sync(0xffffffffu, fix != 1.0f)) {
             // the product of the unit before has to be in O
             ok = mbar_wait(&bars->o[hf], (no - 1) & 1u);
@@ -539,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
               uint32_t v[32], x[16];
-              tmem_load32(o_at + 32 * c, v);
+              tmem_load32_now(o_at + 32 * c, v);
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
 #pragma unroll
@@ -578,11 +676,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
 #pragma unroll
               for (int i = 0; i < 32; ++i) x[32 * c + i] = 0.0f;
               if (any) {
-                tmem_load32(o_at + 32 * c, u);
+                tmem_load32_now(o_at + 32 * c, u);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) x[32 * c + 8 * (i / 8) + v_elem<BITS>(i % 8)] = __uint_as_float(u[i]) * inv;
                 if constexpr (N == 2) {
-                  tmem_load32(o_at + 64 + 32 * c, u);
+                  tmem_load32_now(o_at + 64 + 32 * c, u);
 #pragma unroll
                   for (int i = 0; i < 32; ++i)
                     x[32 * c + 8 * (i / 8) + v_elem<BITS>(i % 8)] += __uint_as_float(u[i]) * (b == 0 ? inv : -inv);
@@ -591,10 +689,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
             }
             reg_stages<64, 0, 6>(x);
             if (mine) {
-              if (a.v_signs != nullptr) {
 #pragma unroll
-                for (int i = 0; i < 64; ++i) x[i] = __ldg(a.v_signs + 64 * b + i) < 0 ? -x[i] : x[i];
-              }
+              for (int i = 0; i < 64; ++i)
+                x[i] = __uint_as_float(__float_as_uint(x[i]) ^ ((v_neg[2 * b + i / 32] << (31 - i % 32)) & 0x80000000u));
               const int64_t at = (g.q.t0 + tok) * t.o_ts + head * t.o_hs + 64 * b;
 #pragma unroll
               for (int i = 0; i < 64; i += 8) {
@@ -607,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
             uint32_t u[32];
-            if (any) tmem_load32(o_at + 32 * c, u);
+            if (any) tmem_load32_now(o_at + 32 * c, u);
             float x[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) x[8 * (i / 8) + v_elem<BITS>(i % 8)] = any ? __uint_as_float(u[i]) : 0.0f;
@@ -635,6 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
     if (threadIdx.x == 0) work.part[2 * blockIdx.x + 1] = open;
   } else if (warp < 12) {
     // ---------------- codes to operands ----------------
+    regs_less<112>();
     w.start(bars);
     const int i = threadIdx.x - 256;
     const int piece = i % CH;
@@ -645,28 +743,38 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
       uint4 kr[CH], vr[CH];
       float ksc = 0.0f, vsc = 0.0f;
       bool in = false;
-      auto vector_of = [&](int j, int tk) {
-        const int64_t p = int64_t(j) * kKeys + tk;
-        const int64_t slot = p < g.q.hi ? kv_slot(a, g.s, p) : -1;
-        return slot < 0 ? slot : slot + (int64_t(g.h) << a.log_page);
-      };
-      auto load = [&](int j, const uint8_t* codes, uint4 (&x)[CH]) {
+      // this thread's vectors of unit j (-1: no such position), and the one whose scales it brings
+      int64_t vec[CH], own;
+      auto find = [&](int j) {
 #pragma unroll
-        for (int k = 0; k < CH; ++k) {
-          const int64_t vec = vector_of(j, i / CH + (128 / CH) * k);
-          x[k] = vec < 0 ? make_uint4(0, 0, 0, 0) : __ldg(reinterpret_cast<const uint4*>(codes + vec * VB + 16 * piece));
+        for (int k = 0; k <= CH; ++k) {
+          const int64_t p = int64_t(j) * kKeys + (k < CH ? i / CH + (128 / CH) * k : i);
+          const int64_t slot = p < g.q.hi ? kv_slot(a, g.s, p) : -1;
+          const int64_t v = slot < 0 ? slot : slot + (int64_t(g.h) << a.log_page);
+          if (k < CH) vec[k] = v;
+          else own = v;
         }
       };
-      auto load_scales = [&](int j) {
-        const int64_t vec = vector_of(j, i);
-        in = vec >= 0;
-        ksc = in ? __ldg(a.k_scales + vec) : 0.0f;
-        vsc = in ? __ldg(a.v_scales + vec) : 0.0f;
+      auto load = [&](const uint8_t* codes, uint4 (&x)[CH]) {
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+          x[k] = make_uint4(0, 0, 0, 0);
+          if (vec[k] >= 0) load16(x[k], codes + vec[k] * VB + 16 * piece);
+        }
+      };
+      auto load_scales = [&]() {
+        in = own >= 0;
+        ksc = vsc = 0.0f;
+        if (in) {
+          load4(ksc, a.k_scales + own);
+          load4(vsc, a.v_scales + own);
+        }
       };
       if (g.ub < g.ue) {
-        load(g.ub, a.k_codes, kr);
-        load_scales(g.ub);
-        load(g.ub, a.v_codes, vr);
+        find(g.ub);
+        load(a.k_codes, kr);
+        load_scales();
+        load(a.v_codes, vr);
       }
       for (int j = g.ub; j < g.ue; ++j, ++kv) {
         const int st = kv & 1;
@@ -719,9 +827,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
         store(smem + F::K + st * F::TILE, kr, false);
         fence_proxy_async_smem();
         mbar_arrive(&bars->kfull[st]);
+        // the next unit's codes are on their way while this one's are waited for and unpacked
         if (j + 1 < g.ue) {
-          load(j + 1, a.k_codes, kr);
-          load_scales(j + 1);
+          find(j + 1);
+          load(a.k_codes, kr);
+          load_scales();
         }
         ok = round == 0 || mbar_wait(&bars->vempty[st], (round - 1) & 1u);
         ok = __all_sync(0xffffffffu, ok);
@@ -729,70 +839,83 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
         store(smem + F::V + st * F::TILE, vr, true);
         fence_proxy_async_smem();
         mbar_arrive(&bars->vfull[st]);
-        if (j + 1 < g.ue) load(j + 1, a.v_codes, vr);
+        if (j + 1 < g.ue) load(a.v_codes, vr);
       }
     }
     if (!ok && !*abort) give_up();
   } else {
-   regs_less<64>();
-   if (warp == 12 && lane == 0) {
-    // ---------------- products ----------------
-    w.start(bars);
-    constexpr uint32_t id_s = instr_desc(false, 128, false), id_o = instr_desc(true, D, true);
-    const uint32_t base = smem_u32(smem);
-    uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
-    uint32_t kv0 = 0;
-    bool ok = true;
-    for (bool more = w.begin(a, t); more && ok; more = w.next(a, t)) {
-      const Segment& g = w.g;
-      for (int j = g.ub - 1; j < g.ue && ok; ++j) {
-        if (g.ub == g.ue) break;
-        const uint32_t kv = kv0 + uint32_t(j - g.ub);  // unit j (j = ub - 1: none)
-        const uint32_t kn = kv + 1;
-        bool have_v = false, have_k = false;
+    regs_less<48>();
+    if (warp == 12) {
+      // ---------------- products: the warp waits, one thread issues ----------------
+      w.start(bars);
+      constexpr uint32_t id_s = instr_desc(false, 128, false), id_o = instr_desc(true, D, true);
+      const uint32_t base = smem_u32(smem);
+      // descriptors of the tiles: the upper word is the same for all, the lower one holds the address
+      const uint64_t dk = desc_sw128(base, 16, 1024), dv = desc_sw128(base + F::V, 16384, 1024);
+      const uint32_t k_hi = uint32_t(dk >> 32), v_hi = uint32_t(dv >> 32);
+      const uint32_t q_lo = uint32_t(dk), k_lo = q_lo + (F::K >> 4), v_lo = uint32_t(dv);
+      uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
+      uint32_t kv0 = 0;
+      bool ok = true;
+      for (bool more = w.begin(a, t); more && ok; more = w.next(a, t)) {
+        const Segment& g = w.g;
+        for (int j = g.ub - 1; j < g.ue && ok; ++j) {
+          if (g.ub == g.ue) break;
+          const uint32_t kv = kv0 + uint32_t(j - g.ub);  // unit j (j = ub - 1: none)
+          const uint32_t kn = kv + 1;
+          bool have_v = false, have_k = false;
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const Half& f = g.half[hf];
-          if (ok && j >= f.js && j < f.je) {
-            if (!have_v) ok = mbar_wait(&bars->vfull[kv & 1], (kv >> 1) & 1u);
-            have_v = true;
-            ok = ok && !*abort && mbar_wait(&bars->p[hf], np[hf] & 1u);
-            if (!ok) break;
-            ++np[hf];
-            fence_after();
+          for (int hf = 0; hf < 2; ++hf) {
+            const Half& f = g.half[hf];
+            if (ok && j >= f.js && j < f.je) {
+              if (!have_v) ok = mbar_wait(&bars->vfull[kv & 1], (kv >> 1) & 1u);
+              have_v = true;
+              ok = ok && !*abort && mbar_wait(&bars->p[hf], np[hf] & 1u);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              ++np[hf];
+              fence_after();
+              if (elect_one()) {
+                const uint32_t lo = v_lo + (kv & 1) * (F::TILE >> 4);
+                const bool add = j > f.js;
 #pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)
-              mma_ts(tmem + F::O_COL + D * hf, tmem + F::S_COL + 128 * hf + 8 * k,
-                     desc_sw128(base + F::V + (kv & 1) * F::TILE + k * 16 * 128, 16384, 1024), id_o, j > f.js || k > 0);
-            commit(&bars->o[hf]);
-          }
-          if (ok && j + 1 >= f.js && j + 1 < f.je) {
-            if (!have_k) ok = mbar_wait(&bars->kfull[kn & 1], (kn >> 1) & 1u);
-            have_k = true;
-            if (ok && j + 1 == f.js) ok = mbar_wait(&bars->q[hf], nq[hf]++ & 1u);
-            if (!ok || *abort) {
-              ok = false;
-              break;
+                for (int k = 0; k < kKeys / 16; ++k)
+                  mma_ts(tmem + F::O_COL + D * hf, tmem + F::S_COL + 128 * hf + 8 * k, lo + k * 128, v_hi, id_o, k > 0 || add);
+                commit(&bars->o[hf]);
+              }
             }
-            fence_after();
+            if (ok && j + 1 >= f.js && j + 1 < f.je) {
+              if (!have_k) ok = mbar_wait(&bars->kfull[kn & 1], (kn >> 1) & 1u);
+              have_k = true;
+              if (ok && j + 1 == f.js) ok = mbar_wait(&bars->q[hf], nq[hf]++ & 1u);
+              ok = __all_sync(0xffffffffu, ok && !*abort);
+              if (!ok) break;
+              fence_after();
+              if (elect_one()) {
+                const uint32_t lo_q = q_lo + hf * (F::TILE >> 4), lo_k = k_lo + (kn & 1) * (F::TILE >> 4);
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-              mma_ss(tmem + F::S_COL + 128 * hf, desc_sw128(base + F::Q + hf * F::TILE + (k / 4) * 16384 + 32 * (k % 4), 16, 1024),
-                     desc_sw128(base + F::K + (kn & 1) * F::TILE + (k / 4) * 16384 + 32 * (k % 4), 16, 1024), id_s, k > 0);
-            commit(&bars->s[hf]);
+                for (int k = 0; k < D / 16; ++k)
+                  mma_ss(tmem + F::S_COL + 128 * hf, lo_q + (k / 4) * 1024 + 2 * (k % 4), lo_k + (k / 4) * 1024 + 2 * (k % 4),
+                         k_hi, id_s, k > 0);
+                commit(&bars->s[hf]);
+              }
+            }
+            __syncwarp();
           }
+          if (!ok) break;
+          if (elect_one()) {
+            if (j >= g.ub) commit(&bars->vempty[kv & 1]);
+            if (j + 1 < g.ue) commit(&bars->kempty[kn & 1]);
+          }
+          __syncwarp();
         }
-        if (!ok) break;
-        if (j >= g.ub) commit(&bars->vempty[kv & 1]);
-        if (j + 1 < g.ue) commit(&bars->kempty[kn & 1]);
+        kv0 += uint32_t(g.ue - g.ub);
       }
-      kv0 += uint32_t(g.ue - g.ub);
+      if (!ok && !*abort) give_up();
+      // every product has ended before tensor memory is given back
+      if (elect_one()) commit(&bars->done);
+      if (!mbar_wait(&bars->done, 0u)) atomicAdd(&g_wait_timeouts_kv, 1u);
     }
-    if (!ok && !*abort) give_up();
-    // every product has ended before tensor memory is given back
-    commit(&bars->done);
-    if (!mbar_wait(&bars->done, 0u)) atomicAdd(&g_wait_timeouts_kv, 1u);
-   }
   }
   __syncwarp();
   fence_before();

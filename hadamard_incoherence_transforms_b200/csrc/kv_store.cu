@@ -74,6 +74,7 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(const KvArgs a, const Kv
   constexpr int LPV = KvLanes<D>::LPV;
   extern __shared__ float2 cs[];  // [tile][n_freq]
   __shared__ Tile tl;
+  __shared__ uint64_t turns[D / 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
   const int64_t t0 = int64_t(blockIdx.x) * tile;
   const int nt = int(min(int64_t(tile), a.tokens - t0));
@@ -81,10 +82,11 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(const KvArgs a, const Kv
     const KvToken k = kv_token(a, t0 + j, lane);
     if (lane == 0) tl.tok[j] = k;
   }
+  kv_turns(a, turns, threadIdx.x, blockDim.x);
   __syncthreads();
   for (int i = threadIdx.x; i < nt * a.n_freq; i += blockDim.x) {
     const int j = i / a.n_freq, f = i - j * a.n_freq;
-    if (tl.tok[j].slot >= 0) cs[i] = kv_angle(a, t0 + j, tl.tok[j].pos, f);
+    if (tl.tok[j].slot >= 0) cs[i] = kv_angle(a, turns, t0 + j, int(tl.tok[j].pos), f);
   }
   __syncthreads();
   const int l = threadIdx.x % LPV;
