@@ -12,10 +12,9 @@
 //                   (bf16, P read from tensor memory where it replaced S).
 // The two halves alternate: while one half's softmax runs, the tensor cores
 // work on the other's products.  Key and value units are converted once for
-// both.  The codes stay exact integers: a key's scale multiplies its column of
-// S, a value's its column of P.  O is rescaled only when a row's maximum has
-// grown by more than 2^8 over the one it is relative to (P then stays below
-// 2^8, which bf16 and the fp32 sums hold as well as values below 1).
+// both, their scales folded in with one rounding (2^-11 of a key, 2^-8 of a
+// value: half the work of the softmax roles went into scales otherwise, see
+// UnitSoftmax for what is left of it).
 #include "kv_codes.cuh"
 #include "kv_split.cuh"
 
@@ -34,17 +33,19 @@ constexpr int kRows = 256;      // query rows of a unit
 constexpr int kKeys = 128;      // positions of a unit
 constexpr int kThreads = 16 * 32;  // warps 13-15 are idle: registers are dealt out to groups of four warps
 constexpr int kCtas = 148;
-constexpr float kGrow = 8.0f;   // growth of a maximum (base 2) that is tolerated
+constexpr float kGrow = 65536.0f;  // sum of 32 probabilities above which a row gets a new reference
 
 template <int D>
 struct Prompt {
   static constexpr int BLK = D / 64;             // 64-element column blocks of an operand
   static constexpr int TILE = BLK * 128 * 128;   // 128 vectors of D 16-bit elements
   static constexpr int Q = 0, K = 2 * TILE, V = 4 * TILE, SC = 6 * TILE;
-  // scale ring: four units of 128 key scales, 128 value scales and a 128-bit mask
-  static constexpr int SC_STAGE = 2 * 128 * 4 + 16;
+  // ring of four units: which positions exist (128 bits), the power of two of the key scales
+  static constexpr int SC_STAGE = 32;
   static constexpr int ES = SC + 4 * SC_STAGE;   // 256 row factors
-  static constexpr int BARS = ES + kRows * 4;
+  static constexpr int TS = ES + kRows * 4;      // two units' scales, and the largest key scale of each warp
+  static constexpr int TS_STAGE = 2 * 128 * 4 + 16;
+  static constexpr int BARS = TS + 2 * TS_STAGE;
   static constexpr int BYTES = BARS + 512 + 1024;
   static constexpr int S_COL = 0, O_COL = 2 * 128;  // tensor memory columns
   static constexpr int COLS = 512;
@@ -367,22 +368,22 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // One row's softmax of a unit: its 128 scores in tensor memory become
-// probabilities times value scales (bf16, in the same place).  m: the maximum
-// they are relative to, l: the sum of probabilities, fix: what sums from before
-// have to be multiplied with.  FULL: every column is seen.
+// probabilities (bf16, in the same place).  m: the reference they are relative
+// to, a maximum of scores seen before; l: the sum of probabilities; fix: what
+// sums from before have to be multiplied with.  FULL: every column is seen.
 //
-// 32 columns at a time, against the maximum so far; where some row's scores
-// exceed it by more than 2^kGrow (or it has none yet) the warp takes the larger
-// one for the rows that need it and brings the columns already done (and, through
-// `fix`, l and O) to it.  The usual unit is one pass over its scores.  The loop
-// is not unrolled: the roles share the instruction cache.
+// 32 columns at a time.  No maximum is taken as long as their probabilities add
+// up to less than kGrow: bf16 and fp32 hold a probability of 2^16 as well as one
+// of 1.  Above it, or while a row has no reference yet, the warp takes the
+// largest score as the reference of the rows concerned and brings the columns
+// already done (and, through `fix`, l and O) to it.  The loop is not unrolled:
+// the roles share the instruction cache.
 template <bool FULL>
 struct UnitSoftmax {
   uint32_t s_at;
-  const float4 *ks, *vs;
   uint4 there;
   int c_lo, c_hi;
-  float qe;
+  float qu;  // the row's and the unit's power of two
 
   __device__ __forceinline__ uint32_t seen(int c) const {  // of columns 32 c .. 32 c + 31
     const uint32_t e = c == 0 ? there.x : c == 1 ? there.y : c == 2 ? there.z : there.w;
@@ -390,52 +391,50 @@ struct UnitSoftmax {
     const uint32_t below = x1 == 32 ? ~0u : (1u << x1) - 1, under = x0 == 32 ? ~0u : (1u << x0) - 1;
     return e & below & ~under;
   }
-  // Base-2 scores of 32 columns below `base`, and the largest.
-  __device__ __forceinline__ float scores(const uint32_t (&v)[32], int c, float base, float (&x)[32]) const {
-    const uint32_t see = FULL ? ~0u : seen(c);
-    float t0 = -INFINITY, t1 = -INFINITY;
+  // Probabilities of 32 columns; their sum.
+  __device__ __forceinline__ float probabilities(const uint32_t (&v)[32], uint32_t see, float base, uint32_t (&p)[16]) const {
+    float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
 #pragma unroll
     for (int i = 0; i < 32; i += 4) {
-      const float4 k = ks[8 * c + i / 4];
+      float x[4];
+      fma_x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]), qu, qu, base, base, x[0], x[1]);
+      fma_x2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]), qu, qu, base, base, x[2], x[3]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[i + e] = __uint_as_float(v[i + e]);
-      mul_x2(x[i], x[i + 1], k.x, k.y);
-      mul_x2(x[i + 2], x[i + 3], k.z, k.w);
-      fma_x2(x[i], x[i + 1], qe, qe, base, base, x[i], x[i + 1]);
-      fma_x2(x[i + 2], x[i + 3], qe, qe, base, base, x[i + 2], x[i + 3]);
-      if constexpr (!FULL) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[i + e] = (see >> (i + e)) & 1 ? x[i + e] : -INFINITY;
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (!FULL) x[e] = (see >> (i + e)) & 1 ? x[e] : -INFINITY;
+        x[e] = ex2(x[e]);
       }
-      t0 = fmaxf(t0, fmaxf(x[i], x[i + 1]));
-      t1 = fmaxf(t1, fmaxf(x[i + 2], x[i + 3]));
+      add_x2(s0, s1, x[0], x[1]);
+      add_x2(s2, s3, x[2], x[3]);
+      p[i / 2] = f32_to_bf16x2(x[0], x[1]);
+      p[i / 2 + 1] = f32_to_bf16x2(x[2], x[3]);
     }
-    return fmaxf(t0, t1);
+    add_x2(s0, s1, s2, s3);
+    return s0 + s1;
   }
   __device__ __forceinline__ void run(float& m, float& l, float& fix) const {
     float base = m == -INFINITY ? 0.0f : -m;
-    float l0 = l, l1 = 0.0f;
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
-      uint32_t v[32];
+      uint32_t v[32], p[16];
       tmem_load32_now(s_at + 32 * c, v);
-      float x[32];
-      const float top = scores(v, c, base, x);
-      const bool grow = top > kGrow || (m == -INFINITY && top > m);
-      if (__any_sync(0xffffffffu, grow)) {
+      const uint32_t see = FULL ? ~0u : seen(c);
+      float sum = probabilities(v, see, base, p);
+      if (__any_sync(0xffffffffu, sum > kGrow || m == -INFINITY)) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) top = (see >> i) & 1 ? fmaxf(top, fmaf(__uint_as_float(v[i]), qu, base)) : top;
+        const bool grow = (m == -INFINITY || sum > kGrow) && top > -INFINITY;
         const float f = grow ? (m == -INFINITY ? 0.0f : ex2(-top)) : 1.0f;
         if (grow) {
           base -= top;
           m = -base;
         }
         fix *= f;
-        l0 *= f;
-        l1 *= f;
-        scores(v, c, base, x);
+        l *= f;
         tmem_store_wait();
 #pragma unroll 1
         for (int k = 0; k < c; ++k) {
-          uint32_t p[16];
           tmem_load16_now(s_at + 16 * k, p);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
@@ -445,28 +444,11 @@ struct UnitSoftmax {
           }
           tmem_store16(s_at + 16 * k, p);
         }
+        sum = probabilities(v, see, base, p);
       }
-      uint32_t p[16];
-      const uint32_t see = FULL ? ~0u : seen(c);
-#pragma unroll
-      for (int i = 0; i < 32; i += 4) {
-        const float4 z = vs[8 * c + i / 4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[i + e] = ex2(x[i + e]);
-        add_x2(l0, l1, x[i], x[i + 1]);
-        add_x2(l0, l1, x[i + 2], x[i + 3]);
-        mul_x2(x[i], x[i + 1], z.x, z.y);
-        mul_x2(x[i + 2], x[i + 3], z.z, z.w);
-        if constexpr (!FULL) {  // the scale of a position that is not seen may be anything
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[i + e] = (see >> (i + e)) & 1 ? x[i + e] : 0.0f;
-        }
-        p[i / 2] = f32_to_bf16x2(x[i], x[i + 1]);
-        p[i / 2 + 1] = f32_to_bf16x2(x[i + 2], x[i + 3]);
-      }
+      l += sum;
       tmem_store16(s_at + 16 * c, p);
     }
-    l = l0 + l1;
   }
 };
 
@@ -612,22 +594,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
         for (int j = f.js; j < f.je && ok; ++j) {
           const uint32_t kv = kv0 + uint32_t(j - g.ub);
           const uint8_t* scp = smem + F::SC + (kv & 3) * F::SC_STAGE;
-          const float4* ks = reinterpret_cast<const float4*>(scp);
-          const float4* vs = ks + 32;
           ok = mbar_wait(&bars->sc[kv & 3], (kv >> 2) & 1u) && mbar_wait(&bars->s[hf], ns & 1u);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           ++ns;
           fence_after();
-          const uint4 there = *reinterpret_cast<const uint4*>(scp + 1024);
+          const uint4 there = *reinterpret_cast<const uint4*>(scp);
+          const float qu = qe * *reinterpret_cast<const float*>(scp + 16);
           const int64_t p0 = int64_t(j) * kKeys;
           const bool full = p0 >= f.lo_max && p0 + kKeys <= f.hi_min && (there.x & there.y & there.z & there.w) == ~0u;
           // columns [c_lo, c_hi) are this row's
           const int c_lo = int(max(int64_t(0), min(int64_t(128), lo - p0)));
           const int c_hi = int(max(int64_t(0), min(int64_t(128), hi - p0)));
           float fix = 1.0f;
-          if (full) UnitSoftmax<true>{s_at, ks, vs, there, 0, kKeys, qe}.run(m, l, fix);
-          else UnitSoftmax<false>{s_at, ks, vs, there, c_lo, c_hi, qe}.run(m, l, fix);
+          if (full) UnitSoftmax<true>{s_at, there, 0, kKeys, qu}.run(m, l, fix);
+          else UnitSoftmax<false>{s_at, there, c_lo, c_hi, qu}.run(m, l, fix);
           if (j > f.js && __any_sync(0xffffffffu, fix != 1.0f)) {
             // the product of the unit before has to be in O
             ok = mbar_wait(&bars->o[hf], (no - 1) & 1u);
@@ -782,18 +763,45 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
         ok = !*abort && (round == 0 || mbar_wait(&bars->kempty[st], (round - 1) & 1u));
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        {  // scales and which positions exist
-          uint8_t* scp = smem + F::SC + (kv & 3) * F::SC_STAGE;
-          reinterpret_cast<float*>(scp)[i] = ksc;
-          reinterpret_cast<float*>(scp)[128 + i] = vsc;
+        // The scales are folded into the operands, with one rounding: a product
+        // with a scale in two parts, hi and the rest.  Keys are relative to a
+        // power of two of the unit's largest scale, so that fp16 holds them.  A
+        // position whose scale is not finite becomes NaN in its scores, and only there.
+        uint8_t* tsp = smem + F::TS + (kv & 1) * F::TS_STAGE;
+        {
+          const bool k_fine = (__float_as_uint(ksc) & 0x7f800000u) != 0x7f800000u;
+          const bool v_fine = (__float_as_uint(vsc) & 0x7f800000u) != 0x7f800000u;
+          reinterpret_cast<float*>(tsp)[i] = v_fine ? ksc : __uint_as_float(0x7fc00000u);
+          reinterpret_cast<float*>(tsp)[128 + i] = v_fine ? vsc : 0.0f;
+          const uint32_t top = __reduce_max_sync(0xffffffffu, k_fine ? __float_as_uint(ksc) & 0x7fffffffu : 0u);
           const uint32_t b = __ballot_sync(0xffffffffu, in);
-          if (lane == 0) reinterpret_cast<uint32_t*>(scp + 1024)[warp - 8] = b;
-          mbar_arrive(&bars->sc[kv & 3]);
+          if (lane == 0) {
+            reinterpret_cast<uint32_t*>(tsp + 1024)[warp - 8] = top;
+            reinterpret_cast<uint32_t*>(smem + F::SC + (kv & 3) * F::SC_STAGE)[warp - 8] = b;
+          }
         }
+        asm volatile("bar.sync 3, 128;" ::: "memory");
+        const uint4 tops = *reinterpret_cast<const uint4*>(tsp + 1024);
+        const uint32_t ex = max(1u, max(max(tops.x, tops.y), max(tops.z, tops.w)) >> 23);
+        const float down = __uint_as_float(ex == 254 ? 0x00400000u : (254 - ex) << 23);
+        if (i == 0) *reinterpret_cast<uint32_t*>(smem + F::SC + (kv & 3) * F::SC_STAGE + 16) = ex << 23;
+        mbar_arrive(&bars->sc[kv & 3]);
         auto store = [&](uint8_t* tile, const uint4 (&x)[CH], bool value) {
 #pragma unroll
           for (int k = 0; k < CH; ++k) {
             const int tk = i / CH + (128 / CH) * k;
+            uint32_t s_hi, s_lo;
+            if (value) {
+              const float sc = reinterpret_cast<const float*>(tsp)[128 + tk];
+              const float hi = __bfloat162float(__float2bfloat16_rn(sc));
+              s_hi = f32_to_bf16x2(hi, hi);
+              s_lo = f32_to_bf16x2(sc - hi, sc - hi);
+            } else {
+              const float sc = reinterpret_cast<const float*>(tsp)[tk] * down;
+              const __half hi = __float2half_rn(sc), lo = __float2half_rn(sc - __half2float(hi));
+              s_hi = uint32_t(__half_as_ushort(hi)) * 0x10001u;
+              s_lo = uint32_t(__half_as_ushort(lo)) * 0x10001u;
+            }
             const uint32_t wd[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
             constexpr int OUT = 128 / (8 * BITS);  // 16-byte chunks of operand from 16 bytes of codes
             const int c0 = OUT * piece;
@@ -803,14 +811,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
 #pragma unroll
             for (int e0 = 0; e0 < OUT; ++e0) {
               uint32_t o[4];
+              const int e = e0 ^ turn;
               if constexpr (BITS == 4) {
-                const int e = e0 ^ turn;
                 const uint32_t u = e == 0 ? wd[0] : e == 1 ? wd[1] : e == 2 ? wd[2] : wd[3];
                 if (value) bf_of4(u, o);
                 else half_of4(u, o);
-                *reinterpret_cast<uint4*>(row + (((c0 % 8) + e) ^ (tk & 7)) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
               } else {
-                const int e = e0 ^ turn;
                 const uint32_t u0 = e == 0 ? wd[0] : wd[2], u1 = e == 0 ? wd[1] : wd[3];
                 if (value) {
                   bf_of8(u0, o[0], o[1]);
@@ -819,8 +825,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
                   half_of8(u0, o[0], o[1]);
                   half_of8(u1, o[2], o[3]);
                 }
-                *reinterpret_cast<uint4*>(row + (((c0 % 8) + e) ^ (tk & 7)) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
               }
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                o[y] = value ? bfma2(o[y], s_hi, bfma2(o[y], s_lo, 0x80008000u)) : hfma2(o[y], s_hi, hfma2(o[y], s_lo, 0x80008000u));
+              *reinterpret_cast<uint4*>(row + (((c0 % 8) + e) ^ (tk & 7)) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
             }
           }
         };

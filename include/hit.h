@@ -402,10 +402,13 @@ HIT_API int harp_blocks(const float* theta, const int8_t* theta_q, float theta_s
  *   sm_scale * (R_k rope(q[t, h])) . (stored key j).  A token at position p
  *   sees j < lens[s], with causal != 0 only j <= p, and with window > 0 (causal
  *   only) only j > p - window.  A token that sees nothing gets 0.  q, out:
- *   [tokens, heads, head_dim], strided as k.  Arithmetic: scores as fp16 x
- *   integer products with fp32 sums (q rounded once to fp16 behind a power of
- *   two of its own row; the codes are exact), softmax in fp32, probabilities
- *   (times the value's scale) rounded once to bf16, fp32 sums.  max_new: an
+ *   [tokens, heads, head_dim], strided as k.  Arithmetic: queries (behind a
+ *   power of two of their own row) fp16, scores and outputs summed in fp32,
+ *   softmax in fp32, probabilities bf16.  Where a sequence has at most 16 query
+ *   rows (tokens * heads / kv_heads) for a key/value head, or head_dim is 256,
+ *   codes and scales enter exactly; in longer chunks keys are rounded once to
+ *   fp16 and values once to bf16, as an unquantized cache would hold them.
+ *   max_new: an
  *   upper bound of n_s (any value >= 1 is right; a tight one saves a launch).
  *   Needs rht_kv_workspace_bytes(heads, kv_heads, head_dim) bytes of 16-byte
  *   aligned workspace, which calls that may run at the same time must not share.

@@ -330,8 +330,8 @@ def test_append_attend_and_read_together():
                     w = np.exp(z - z.max())
                     w /= w.sum()
                     ref = w @ vs[:p + 1, h // g]
-                    bound = (2 * 2.0 ** -11 * (np.abs(kc.rotate(ks[:p + 1, h // g], c.k_signs))
-                                               @ np.abs(kc.rotate(x, c.k_signs))).max() * d ** -0.5 + UBF + 2.0 ** -14)
+                    bound = (4 * 2.0 ** -11 * (np.abs(kc.rotate(ks[:p + 1, h // g], c.k_signs))
+                                               @ np.abs(kc.rotate(x, c.k_signs))).max() * d ** -0.5 + 2 * UBF + 2.0 ** -14)
                     bound = bound * (w @ np.linalg.norm(vs[:p + 1, h // g], axis=1)) + UBF * np.linalg.norm(ref)
                     assert np.linalg.norm(out[row, h].double().cpu().numpy() - ref) <= bound
     # values and keys of the cache stand for what went in, to the codes' half step
