@@ -8,6 +8,7 @@
 //   warps 8-11      codes to fp16 keys and bf16 values in shared memory (128-byte
 //                   swizzle), a two-stage ring each, the next unit's codes on
 //                   their way in registers;
+//   warp 13         finds the CTA's segments and hands them to the others;
 //   warp 12         one thread issues the products: S = Q K^T (fp16), O += P V
 //                   (bf16, P read from tensor memory where it replaced S).
 // The two halves alternate: while one half's softmax runs, the tensor cores
@@ -31,7 +32,7 @@ namespace {
 
 constexpr int kRows = 256;      // query rows of a unit
 constexpr int kKeys = 128;      // positions of a unit
-constexpr int kThreads = 16 * 32;  // warps 13-15 are idle: registers are dealt out to groups of four warps
+constexpr int kThreads = 16 * 32;  // warps 14 and 15 are idle: registers are dealt out to groups of four warps
 constexpr int kCtas = 148;
 constexpr float kGrow = 65536.0f;  // sum of 32 probabilities above which a row gets a new reference
 
@@ -43,9 +44,8 @@ struct Prompt {
   // ring of four units: which positions exist (128 bits), the power of two of the key scales
   static constexpr int SC_STAGE = 32;
   static constexpr int ES = SC + 4 * SC_STAGE;   // 256 row factors
-  static constexpr int TS = ES + kRows * 4;      // two units' scales, and the largest key scale of each warp
-  static constexpr int TS_STAGE = 2 * 128 * 4 + 16;
-  static constexpr int BARS = TS + 2 * TS_STAGE;
+  static constexpr int TS = ES + kRows * 4;      // the largest key scale of each unpacking warp, two units
+  static constexpr int BARS = TS + 32;
   static constexpr int BYTES = BARS + 512 + 1024;
   static constexpr int S_COL = 0, O_COL = 2 * 128;  // tensor memory columns
   static constexpr int COLS = 512;
@@ -179,83 +179,112 @@ __device__ __forceinline__ void plan_warp(const KvArgs& a, const KvAttn& t, Bars
 }
 
 // Half of a segment's rows: the units [js, je) that its rows may see there, and
-// the bounds inside which every row sees everything.
+// the positions [lo_max, hi_min) that all of them see.
 struct Half {
-  int rows, js, je;
+  int rows, js, je, pad;
   int64_t lo_max, hi_min;
 };
-// A CTA's part of one (sequence, head, row tile); every role walks the same ones.
+// A CTA's part of one (sequence, head, row tile).  One warp walks the CTA's
+// share and hands the segments to the other roles through shared memory.
 struct Segment {
-  KvSeq q;
-  int s, h, rt;
-  int row0, nr;
-  int first, count;      // units of the row tile
-  int x0, x1;            // of them, this CTA's
+  int64_t t0, pos0, hi;  // of the sequence: first token, its position, positions that can exist
+  int s, h, row0, nr;
   int ub, ue;            // units that either half needs
+  int begins, whole;     // the row tile begins here; it begins and ends here
+  int last;              // last CTA of the row tile
+  int valid;             // 0: no more segments
   Half half[2];
 };
-struct Walk {
-  Segment g;
-  int64_t left;
-  __device__ __forceinline__ void start(const Bars* b) {
-    left = b->units;
-    g.s = b->seq;
-    g.h = b->h;
-    g.rt = b->rt;
-    g.x0 = b->x0;
-  }
-  __device__ __forceinline__ void fill(const KvArgs& a, const KvAttn& t) {
-    tile_units(t, g.q, g.rt, g.first, g.count);
-    g.x1 = int(min(int64_t(g.count), g.x0 + left));
-    g.row0 = g.rt * kRows;
-    g.nr = int(min(int64_t(kRows), int64_t(g.q.n) * t.group - g.row0));
-    g.ub = INT32_MAX;
-    g.ue = 0;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      Half& f = g.half[k];
-      f.rows = min(128, max(0, g.nr - 128 * k));
-      f.js = f.je = 0;
-      f.lo_max = f.hi_min = 0;
-      if (f.rows > 0) {
-        const int64_t i0 = (g.row0 + 128 * k) / t.group, i1 = (g.row0 + 128 * k + f.rows - 1) / t.group;
-        const int64_t hi = t.causal ? max(int64_t(0), min(g.q.hi, g.q.pos0 + i1 + 1)) : g.q.hi;
-        const int64_t lo = t.window > 0 ? min(hi, max(int64_t(0), g.q.pos0 + i0 - t.window + 1)) : 0;
-        f.hi_min = t.causal ? min(g.q.hi, g.q.pos0 + i0 + 1) : g.q.hi;
-        f.lo_max = t.window > 0 ? g.q.pos0 + i1 - t.window + 1 : 0;
-        f.js = max(g.first + g.x0, int(lo / kKeys));
-        f.je = min(g.first + g.x1, int((hi + kKeys - 1) / kKeys));
-        if (f.js < f.je) {
-          g.ub = min(g.ub, f.js);
-          g.ue = max(g.ue, f.je);
-        } else {
-          f.je = f.js;
+constexpr int kSegments = 4;
+struct SegmentRing {
+  Segment seg[kSegments];
+  uint64_t full[kSegments], empty[kSegments];
+};
+
+// The walk over the share: segments into the ring, then one that ends it.
+// True unless a wait ran out.
+__device__ __forceinline__ bool walk(const KvArgs& a, const KvAttn& t, const Bars* b, SegmentRing* ring,
+                                     volatile int* abort) {
+  int s = b->seq, h = b->h, rt = b->rt, x0 = b->x0;
+  int64_t left = b->units, at = int64_t(blockIdx.x) * b->total / b->ctas;
+  KvSeq q{};
+  if (left > 0) q = kv_seq<kRows, kKeys>(a, t, s);
+  for (int n = 0;; ++n) {
+    if (n >= kSegments && !mbar_wait(&ring->empty[n % kSegments], uint32_t(n / kSegments - 1) & 1u)) return false;
+    if (*abort) return true;
+    Segment& g = ring->seg[n % kSegments];
+    g.valid = left > 0;
+    if (left > 0) {
+      int first, count;
+      tile_units(t, q, rt, first, count);
+      const int x1 = int(min(int64_t(count), x0 + left));
+      g.t0 = q.t0;
+      g.pos0 = q.pos0;
+      g.hi = q.hi;
+      g.s = s;
+      g.h = h;
+      g.row0 = rt * kRows;
+      g.nr = int(min(int64_t(kRows), int64_t(q.n) * t.group - g.row0));
+      int ub = INT32_MAX, ue = 0;
+      for (int k = 0; k < 2; ++k) {
+        Half f{min(128, max(0, g.nr - 128 * k)), 0, 0, 0, 0, 0};
+        if (f.rows > 0) {
+          const int64_t i0 = (g.row0 + 128 * k) / t.group, i1 = (g.row0 + 128 * k + f.rows - 1) / t.group;
+          const int64_t hi = t.causal ? max(int64_t(0), min(q.hi, q.pos0 + i1 + 1)) : q.hi;
+          const int64_t lo = t.window > 0 ? min(hi, max(int64_t(0), q.pos0 + i0 - t.window + 1)) : 0;
+          f.hi_min = t.causal ? min(q.hi, q.pos0 + i0 + 1) : q.hi;
+          f.lo_max = t.window > 0 ? q.pos0 + i1 - t.window + 1 : 0;
+          f.js = max(first + x0, int(lo / kKeys));
+          f.je = min(first + x1, int((hi + kKeys - 1) / kKeys));
+          if (f.js < f.je) {
+            ub = min(ub, f.js);
+            ue = max(ue, f.je);
+          } else {
+            f.je = f.js;
+          }
+        }
+        g.half[k] = f;
+      }
+      g.ub = ub < ue ? ub : 0;
+      g.ue = ub < ue ? ue : 0;
+      g.begins = x0 == 0;
+      g.whole = x0 == 0 && x1 == count;
+      g.last = kv_cta_of(at - x0 + count - 1, b->total, b->ctas);
+      at += x1 - x0;
+      left -= x1 - x0;
+      if (left > 0) {
+        x0 = 0;
+        if (++rt == q.row_tiles) {
+          rt = 0;
+          if (++h == a.hk) {
+            h = 0;
+            do {
+              q = kv_seq<kRows, kKeys>(a, t, ++s);
+            } while (q.n == 0 || !kv_mine(t, q));
+          }
         }
       }
     }
-    if (g.ub > g.ue) g.ub = g.ue = 0;
+    mbar_arrive(&ring->full[n % kSegments]);
+    if (!g.valid) return true;
   }
-  __device__ __forceinline__ bool begin(const KvArgs& a, const KvAttn& t) {
-    if (left <= 0) return false;
-    g.q = kv_seq<kRows, kKeys>(a, t, g.s);
-    fill(a, t);
-    return true;
-  }
-  __device__ __forceinline__ bool next(const KvArgs& a, const KvAttn& t) {
-    left -= g.x1 - g.x0;
-    if (left <= 0) return false;
-    g.x0 = 0;
-    if (++g.rt == g.q.row_tiles) {
-      g.rt = 0;
-      if (++g.h == a.hk) {
-        g.h = 0;
-        do {
-          g.q = kv_seq<kRows, kKeys>(a, t, ++g.s);
-        } while (g.q.n == 0 || !kv_mine(t, g.q));
-      }
+}
+
+// A role's view of the ring; next() is called by whole warps.
+struct Follow {
+  SegmentRing* ring;
+  int n = -1;
+  __device__ __forceinline__ const Segment& seg() const { return ring->seg[n % kSegments]; }
+  // 1: a segment, 0: no more, -1: a wait ran out
+  __device__ __forceinline__ int next(int lane) {
+    if (n >= 0) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ring->empty[n % kSegments]);
     }
-    fill(a, t);
-    return true;
+    ++n;
+    const bool ok = mbar_wait(&ring->full[n % kSegments], uint32_t(n / kSegments) & 1u);
+    if (!__all_sync(0xffffffffu, ok)) return -1;
+    return seg().valid ? 1 : 0;
   }
 };
 
@@ -342,11 +371,14 @@ __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::aft
 __device__ __forceinline__ void load16(uint4& x, const void* p) {
   asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(p));
 }
+__device__ __forceinline__ void load4(int& x, const int* p) {
+  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(x) : "l"(p));
+}
 __device__ __forceinline__ void load4(float& x, const float* p) {
   asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(x) : "l"(p));
 }
 // Registers of a group of four warps (all four run it).  The kernel starts with
-// 128 a thread; 2 x 176 + 112 + 48 are the same 512.
+// 128 a thread; 2 x 160 + 112 + 80 are the same 512.
 template <int N>
 __device__ __forceinline__ void regs_more() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -354,12 +386,6 @@ __device__ __forceinline__ void regs_more() {
 template <int N>
 __device__ __forceinline__ void regs_less() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-// {a0, a1} += {b0, b1}
-__device__ __forceinline__ void add_x2(float& a0, float& a1, float b0, float b1) {
-  unsigned long long A = pk2(a0, a1), B = pk2(b0, b1), R;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(R) : "l"(A), "l"(B));
-  upk2(R, a0, a1);
 }
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -372,15 +398,15 @@ __device__ __forceinline__ float ex2(float x) {
 // to, a maximum of scores seen before; l: the sum of probabilities; fix: what
 // sums from before have to be multiplied with.  FULL: every column is seen.
 //
-// 32 columns at a time.  No maximum is taken as long as their probabilities add
-// up to less than kGrow: bf16 and fp32 hold a probability of 2^16 as well as one
-// of 1.  Above it, or while a row has no reference yet, the warp takes the
-// largest score as the reference of the rows concerned and brings the columns
-// already done (and, through `fix`, l and O) to it.  The loop is not unrolled:
-// the roles share the instruction cache.
+// 32 columns at a time, stored as soon as they are done (holding all of them
+// costs more registers than the roles leave).  No maximum is taken as long as a
+// row's probabilities add up to less than kGrow: bf16 and fp32 hold a probability
+// of 2^16 as well as one of 1.  Above it, or while a row has no reference yet, the
+// largest score becomes the reference of the rows concerned, and the columns
+// already stored (and, through `fix`, l and O) are brought to it.
 template <bool FULL>
 struct UnitSoftmax {
-  uint32_t s_at;
+  uint32_t s_at, p_at;  // tensor memory of the scores and of the probabilities
   uint4 there;
   int c_lo, c_hi;
   float qu;  // the row's and the unit's power of two
@@ -391,63 +417,103 @@ struct UnitSoftmax {
     const uint32_t below = x1 == 32 ? ~0u : (1u << x1) - 1, under = x0 == 32 ? ~0u : (1u << x0) - 1;
     return e & below & ~under;
   }
-  // Probabilities of 32 columns; their sum.
-  __device__ __forceinline__ float probabilities(const uint32_t (&v)[32], uint32_t see, float base, uint32_t (&p)[16]) const {
-    float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 32; i += 4) {
-      float x[4];
-      fma_x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]), qu, qu, base, base, x[0], x[1]);
-      fma_x2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]), qu, qu, base, base, x[2], x[3]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if constexpr (!FULL) x[e] = (see >> (i + e)) & 1 ? x[e] : -INFINITY;
-        x[e] = ex2(x[e]);
+  // Probabilities of 32 columns, packed, and their sum.  The exponential unit
+  // takes a warp's instruction every 8 cycles, and a warp issues in order: the
+  // other work of the neighbouring columns is placed between two exponentials
+  // (volatile, so that it stays there), else its time adds to theirs.
+  __device__ __forceinline__ float probabilities(const uint32_t (&v)[32], uint32_t see, unsigned long long qu2,
+                                                 unsigned long long base2, uint32_t (&p)[16]) const {
+    unsigned long long sum[2] = {0, 0};
+    float x[2][4];  // exponents of these and the next four columns
+    float e[2][4];  // probabilities of these and the four before
+    auto exponents = [&](int g, int h, float (&y)[4]) {  // columns 4 g + 2 h, + 1
+      const int i = 4 * g + 2 * h;
+      unsigned long long r;
+      asm volatile("fma.rn.f32x2 %0, %1, %2, %3;"
+                   : "=l"(r)
+                   : "l"(pk2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]))), "l"(qu2), "l"(base2));
+      upk2(r, y[2 * h], y[2 * h + 1]);
+      if constexpr (!FULL) {
+        y[2 * h] = (see >> i) & 1 ? y[2 * h] : -INFINITY;
+        y[2 * h + 1] = (see >> i) & 2 ? y[2 * h + 1] : -INFINITY;
       }
-      add_x2(s0, s1, x[0], x[1]);
-      add_x2(s2, s3, x[2], x[3]);
-      p[i / 2] = f32_to_bf16x2(x[0], x[1]);
-      p[i / 2 + 1] = f32_to_bf16x2(x[2], x[3]);
+    };
+    auto finish = [&](int g, int h, const float (&y)[4]) {
+      asm volatile("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[h]) : "l"(pk2(y[2 * h], y[2 * h + 1])));
+      asm volatile("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[2 * g + h]) : "f"(y[2 * h + 1]), "f"(y[2 * h]));
+    };
+    auto power = [](float y) {
+      float r;
+      asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
+      return r;
+    };
+    exponents(0, 0, x[0]);
+    exponents(0, 1, x[0]);
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+      float(&now)[4] = x[g & 1];
+      float(&next)[4] = x[(g + 1) & 1];
+      float(&made)[4] = e[g & 1];
+      float(&before)[4] = e[(g + 1) & 1];
+      made[0] = power(now[0]);
+      if (g < 7) exponents(g + 1, 0, next);
+      made[1] = power(now[1]);
+      if (g < 7) exponents(g + 1, 1, next);
+      made[2] = power(now[2]);
+      if (g > 0) finish(g - 1, 0, before);
+      made[3] = power(now[3]);
+      if (g > 0) finish(g - 1, 1, before);
     }
-    add_x2(s0, s1, s2, s3);
-    return s0 + s1;
+    finish(7, 0, e[1]);
+    finish(7, 1, e[1]);
+    float s0, s1, s2, s3;
+    upk2(sum[0], s0, s1);
+    upk2(sum[1], s2, s3);
+    return (s0 + s1) + (s2 + s3);
   }
   __device__ __forceinline__ void run(float& m, float& l, float& fix) const {
     float base = m == -INFINITY ? 0.0f : -m;
-#pragma unroll 1
+    const unsigned long long qu2 = pk2(qu, qu);
+    unsigned long long base2 = pk2(base, base);
+    uint32_t v[2][32];
+    tmem_load32(s_at, v[0]);
+#pragma unroll
     for (int c = 0; c < 4; ++c) {
-      uint32_t v[32], p[16];
-      tmem_load32_now(s_at + 32 * c, v);
+      const uint32_t(&w)[32] = v[c & 1];
+      tmem_load_wait(v[c & 1]);
+      if (c < 3) tmem_load32(s_at + 32 * c + 32, v[(c + 1) & 1]);
       const uint32_t see = FULL ? ~0u : seen(c);
-      float sum = probabilities(v, see, base, p);
-      if (__any_sync(0xffffffffu, sum > kGrow || m == -INFINITY)) {
+      uint32_t p[16];
+      float sum;
+#pragma unroll 1
+      for (bool again = false;; again = true) {
+        sum = probabilities(w, see, qu2, base2, p);
+        if (again || !__any_sync(0xffffffffu, sum > kGrow || m == -INFINITY)) break;
         float top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) top = (see >> i) & 1 ? fmaxf(top, fmaf(__uint_as_float(v[i]), qu, base)) : top;
-        const bool grow = (m == -INFINITY || sum > kGrow) && top > -INFINITY;
-        const float f = grow ? (m == -INFINITY ? 0.0f : ex2(-top)) : 1.0f;
-        if (grow) {
-          base -= top;
-          m = -base;
-        }
+        for (int i = 0; i < 32; ++i) top = FULL || (see >> i) & 1 ? fmaxf(top, __uint_as_float(w[i])) : top;
+        top *= qu;
+        const bool grow = m == -INFINITY ? top > m : sum > kGrow;
+        const float f = grow ? ex2(m - top) : 1.0f;  // 0 for a first reference
+        if (grow) m = top, base = -top;
+        base2 = pk2(base, base);
         fix *= f;
         l *= f;
         tmem_store_wait();
 #pragma unroll 1
         for (int k = 0; k < c; ++k) {
-          tmem_load16_now(s_at + 16 * k, p);
+          tmem_load16_now(p_at + 16 * k, p);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            float u, w;
-            bf16x2_to_f32(p[i], u, w);
-            p[i] = f32_to_bf16x2(u * f, w * f);
+            float y0, y1;
+            bf16x2_to_f32(p[i], y0, y1);
+            p[i] = f32_to_bf16x2(y0 * f, y1 * f);
           }
-          tmem_store16(s_at + 16 * k, p);
+          tmem_store16(p_at + 16 * k, p);
         }
-        sum = probabilities(v, see, base, p);
       }
       l += sum;
-      tmem_store16(s_at + 16 * c, p);
+      tmem_store16(p_at + 16 * c, p);
     }
   }
 };
@@ -462,12 +528,13 @@ __host__ __device__ constexpr int v_elem(int c) {
 template <int D, int BITS>
 __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const KvAttn t) {
   using F = Prompt<D>;
-  constexpr int VB = D * BITS / 8, CH = VB / 16;
+  constexpr int VB = D * BITS / 8, CH = VB / 16;  // bytes and 16-byte pieces of a vector's codes
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Bars* bars = reinterpret_cast<Bars*>(smem + F::BARS);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &bars->abort;
+  __shared__ SegmentRing ring;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -481,6 +548,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
       mbar_init(&bars->o[i], 1);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&bars->sc[i], 128);
+    for (int i = 0; i < kSegments; ++i) {
+      mbar_init(&ring.full[i], 1);
+      mbar_init(&ring.empty[i], 13);  // 8 softmax, 4 unpacking, 1 issuing warps
+    }
     mbar_init(&bars->done, 1);
     bars->abort = 0;
     mbar_init_fence();
@@ -510,10 +581,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
     *abort = 1;
   };
 
-  Walk w;
+  Follow w{&ring};
+  int more = 1;
   if (warp < 8) {
-    regs_more<176>();
-    w.start(bars);
+    regs_more<160>();
     // ---------------- softmax of half `hf`, a thread a row ----------------
     const int hf = warp >> 2, r = threadIdx.x & 127;
     const uint32_t lane_at = tmem + (uint32_t(32 * (warp & 3)) << 16);
@@ -524,11 +595,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
     uint32_t kv0 = 0;         // units converted before this segment
     KvPart open;
     open.first = -1;
-    int64_t unit = w.left;    // of the CTA's share, what is left before this segment
-    for (bool more = w.begin(a, t); more && !*abort; more = w.next(a, t)) {
-      const Segment& g = w.g;
-      const Half& f = g.half[hf];
-      const int row = g.row0 + 128 * hf + r;
+    while (!__any_sync(0xffffffffu, *abort) && (more = w.next(lane)) > 0) {
+      const Segment& g = w.seg();
+      const Half f = g.half[hf];
+      const int ub = g.ub, row = g.row0 + 128 * hf + r;
       const bool mine = r < f.rows;
       const int tok = mine ? row / t.group : 0;
       const int head = g.h * t.group + (mine ? row - tok * t.group : 0);
@@ -546,15 +616,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
           for (int i = 0; i < 32; ++i) x[i] = 0.0f;
           if (qr < f.rows) {
             const int row_q = g.row0 + 128 * hf + qr, tk = row_q / t.group;
-            const int64_t src = (g.q.t0 + tk) * t.q_ts + (int64_t(g.h) * t.group + row_q - tk * t.group) * t.q_hs;
+            const int64_t src = (g.t0 + tk) * t.q_ts + (int64_t(g.h) * t.group + row_q - tk * t.group) * t.q_hs;
             if (t.q_f32) {
 #pragma unroll
               for (int c = 0; c < 4; ++c) kv_load8<true>(t.q, src + 8 * (c * LPV + ln), x + 8 * c);
-              if (a.n_freq > 0) kv_rope_direct<D, true>(x, t.q, src, a, turns, g.q.t0 + tk, int(g.q.pos0) + tk, ln);
+              if (a.n_freq > 0) kv_rope_direct<D, true>(x, t.q, src, a, turns, g.t0 + tk, int(g.pos0) + tk, ln);
             } else {
 #pragma unroll
               for (int c = 0; c < 4; ++c) kv_load8<false>(t.q, src + 8 * (c * LPV + ln), x + 8 * c);
-              if (a.n_freq > 0) kv_rope_direct<D, false>(x, t.q, src, a, turns, g.q.t0 + tk, int(g.q.pos0) + tk, ln);
+              if (a.n_freq > 0) kv_rope_direct<D, false>(x, t.q, src, a, turns, g.t0 + tk, int(g.pos0) + tk, ln);
             }
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -587,12 +657,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
         mbar_arrive(&bars->q[hf]);
         asm volatile("bar.sync %0, 128;" ::"r"(1 + hf) : "memory");
         const float qe = es[r];
-        const int64_t pos = g.q.pos0 + tok;
-        const int64_t hi = mine ? (t.causal ? min(g.q.hi, pos + 1) : g.q.hi) : 0;
+        const int64_t pos = g.pos0 + tok;
+        const int64_t hi = mine ? (t.causal ? min(g.hi, pos + 1) : g.hi) : 0;
         const int64_t lo = t.window > 0 ? pos - t.window + 1 : 0;
 
         for (int j = f.js; j < f.je && ok; ++j) {
-          const uint32_t kv = kv0 + uint32_t(j - g.ub);
+          const uint32_t kv = kv0 + uint32_t(j - ub);
           const uint8_t* scp = smem + F::SC + (kv & 3) * F::SC_STAGE;
           ok = mbar_wait(&bars->sc[kv & 3], (kv >> 2) & 1u) && mbar_wait(&bars->s[hf], ns & 1u);
           ok = __all_sync(0xffffffffu, ok);
@@ -607,8 +677,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
           const int c_lo = int(max(int64_t(0), min(int64_t(128), lo - p0)));
           const int c_hi = int(max(int64_t(0), min(int64_t(128), hi - p0)));
           float fix = 1.0f;
-          if (full) UnitSoftmax<true>{s_at, there, 0, kKeys, qu}.run(m, l, fix);
-          else UnitSoftmax<false>{s_at, there, c_lo, c_hi, qu}.run(m, l, fix);
+          if (full) UnitSoftmax<true>{s_at, s_at, there, 0, kKeys, qu}.run(m, l, fix);
+          else UnitSoftmax<false>{s_at, s_at, there, c_lo, c_hi, qu}.run(m, l, fix);
           if (j > f.js && __any_sync(0xffffffffu, fix != 1.0f)) {
             // the product of the unit before has to be in O
             ok = mbar_wait(&bars->o[hf], (no - 1) & 1u);
@@ -641,12 +711,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
         fence_after();
       }
       // ---------------- the half's result ----------------
-      const bool whole = g.x0 == 0 && g.x1 == g.count;
       const bool any = f.js < f.je;
-      const size_t slot_row = (g.x0 == 0 ? 2 * size_t(blockIdx.x) + 1 : 2 * size_t(blockIdx.x)) * kRows + 128 * hf + r;
+      const size_t slot_row = (2 * size_t(blockIdx.x) + (g.begins ? 1 : 0)) * kRows + 128 * hf + r;
       const float inv = l == 0.0f ? 0.0f : (D == 64 ? 0.125f : 0.08838834764831845f) / l;
       if (f.rows > 0) {  // by the whole warp: tensor memory is read together
-        if (whole) {
+        if (g.whole) {
           constexpr int N = D / 64;  // the transform's last stage joins the halves of 128 elements
 #pragma unroll 1
           for (int b = 0; b < N; ++b) {
@@ -673,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
 #pragma unroll
               for (int i = 0; i < 64; ++i)
                 x[i] = __uint_as_float(__float_as_uint(x[i]) ^ ((v_neg[2 * b + i / 32] << (31 - i % 32)) & 0x80000000u));
-              const int64_t at = (g.q.t0 + tok) * t.o_ts + head * t.o_hs + 64 * b;
+              const int64_t at = (g.t0 + tok) * t.o_ts + head * t.o_hs + 64 * b;
 #pragma unroll
               for (int i = 0; i < 64; i += 8) {
                 if (t.o_f32) kv_store8<true>(t.out, at + i, x + i);
@@ -697,69 +766,70 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
           if (mine) work.ms[slot_row] = make_float2(m, l);
         }
       }
-      if (!whole && g.x0 == 0) {
-        const int64_t at = int64_t(blockIdx.x) * bars->total / bars->ctas + (unit - w.left);
+      if (g.begins && !g.whole) {
         open.first = blockIdx.x;
-        open.last = kv_cta_of(at + g.count - 1, bars->total, bars->ctas);
+        open.last = g.last;
         open.rows = g.nr;
         open.row0 = g.row0;
-        open.t0 = g.q.t0;
+        open.t0 = g.t0;
         open.h = g.h;
         open.pad = 0;
       }
       fence_before();
       kv0 += uint32_t(g.ue - g.ub);
     }
+    if (more < 0 && lane == 0) give_up();
     if (threadIdx.x == 0) work.part[2 * blockIdx.x + 1] = open;
   } else if (warp < 12) {
-    // ---------------- codes to operands ----------------
+    // ---------------- codes to operands, a thread a position ----------------
     regs_less<112>();
-    w.start(bars);
     const int i = threadIdx.x - 256;
-    const int piece = i % CH;
     uint32_t kv = 0;
     bool ok = true;
-    for (bool more = w.begin(a, t); more && ok; more = w.next(a, t)) {
-      const Segment& g = w.g;
+    while (ok && (more = w.next(lane)) > 0) {
+      const int ub = w.seg().ub, ue = w.seg().ue, h = w.seg().h;
+      const int64_t hi = w.seg().hi;
+      const int32_t* const pages = a.table + int64_t(w.seg().s) * a.ld_table;
       uint4 kr[CH], vr[CH];
       float ksc = 0.0f, vsc = 0.0f;
       bool in = false;
-      // this thread's vectors of unit j (-1: no such position), and the one whose scales it brings
-      int64_t vec[CH], own;
-      auto find = [&](int j) {
-#pragma unroll
-        for (int k = 0; k <= CH; ++k) {
-          const int64_t p = int64_t(j) * kKeys + (k < CH ? i / CH + (128 / CH) * k : i);
-          const int64_t slot = p < g.q.hi ? kv_slot(a, g.s, p) : -1;
-          const int64_t v = slot < 0 ? slot : slot + (int64_t(g.h) << a.log_page);
-          if (k < CH) vec[k] = v;
-          else own = v;
-        }
+      // the page of this thread's position in unit j (-1: there is none), and its vector in that page
+      auto page_of = [&](int j) {
+        const int64_t p = int64_t(j) * kKeys + i;
+        int page = -1;
+        if (j < ue && p < hi) load4(page, pages + (p >> a.log_page));
+        return page;
       };
-      auto load = [&](const uint8_t* codes, uint4 (&x)[CH]) {
+      auto vector_of = [&](int j, int page) {
+        const int64_t p = int64_t(j) * kKeys + i;
+        in = page >= 0 && page < a.pages;
+        return (((int64_t(page) * a.hk + h) << a.log_page) + (p & ((int64_t(1) << a.log_page) - 1)));
+      };
+      auto load = [&](const uint8_t* codes, int64_t vec, uint4 (&x)[CH]) {
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
           x[k] = make_uint4(0, 0, 0, 0);
-          if (vec[k] >= 0) load16(x[k], codes + vec[k] * VB + 16 * piece);
+          if (in) load16(x[k], codes + vec * VB + 16 * k);
         }
       };
-      auto load_scales = [&]() {
-        in = own >= 0;
+      auto load_scales = [&](int64_t vec) {
         ksc = vsc = 0.0f;
         if (in) {
-          load4(ksc, a.k_scales + own);
-          load4(vsc, a.v_scales + own);
+          load4(ksc, a.k_scales + vec);
+          load4(vsc, a.v_scales + vec);
         }
       };
-      if (g.ub < g.ue) {
-        find(g.ub);
-        load(a.k_codes, kr);
-        load_scales();
-        load(a.v_codes, vr);
+      int64_t vec = 0;
+      if (ub < ue) {
+        vec = vector_of(ub, page_of(ub));
+        load_scales(vec);
+        load(a.k_codes, vec, kr);
+        load(a.v_codes, vec, vr);
       }
-      for (int j = g.ub; j < g.ue; ++j, ++kv) {
+      for (int j = ub; j < ue; ++j, ++kv) {
         const int st = kv & 1;
         const uint32_t round = kv >> 1;
+        const int page = page_of(j + 1);
         ok = !*abort && (round == 0 || mbar_wait(&bars->kempty[st], (round - 1) & 1u));
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -767,96 +837,85 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
         // with a scale in two parts, hi and the rest.  Keys are relative to a
         // power of two of the unit's largest scale, so that fp16 holds them.  A
         // position whose scale is not finite becomes NaN in its scores, and only there.
-        uint8_t* tsp = smem + F::TS + (kv & 1) * F::TS_STAGE;
+        uint32_t* const tops = reinterpret_cast<uint32_t*>(smem + F::TS + (kv & 1) * 16);
+        uint8_t* const scp = smem + F::SC + (kv & 3) * F::SC_STAGE;
+        const bool k_fine = (__float_as_uint(ksc) & 0x7f800000u) != 0x7f800000u;
+        const bool v_fine = (__float_as_uint(vsc) & 0x7f800000u) != 0x7f800000u;
         {
-          const bool k_fine = (__float_as_uint(ksc) & 0x7f800000u) != 0x7f800000u;
-          const bool v_fine = (__float_as_uint(vsc) & 0x7f800000u) != 0x7f800000u;
-          reinterpret_cast<float*>(tsp)[i] = v_fine ? ksc : __uint_as_float(0x7fc00000u);
-          reinterpret_cast<float*>(tsp)[128 + i] = v_fine ? vsc : 0.0f;
           const uint32_t top = __reduce_max_sync(0xffffffffu, k_fine ? __float_as_uint(ksc) & 0x7fffffffu : 0u);
           const uint32_t b = __ballot_sync(0xffffffffu, in);
           if (lane == 0) {
-            reinterpret_cast<uint32_t*>(tsp + 1024)[warp - 8] = top;
-            reinterpret_cast<uint32_t*>(smem + F::SC + (kv & 3) * F::SC_STAGE)[warp - 8] = b;
+            tops[warp - 8] = top;
+            reinterpret_cast<uint32_t*>(scp)[warp - 8] = b;
           }
         }
         asm volatile("bar.sync 3, 128;" ::: "memory");
-        const uint4 tops = *reinterpret_cast<const uint4*>(tsp + 1024);
-        const uint32_t ex = max(1u, max(max(tops.x, tops.y), max(tops.z, tops.w)) >> 23);
+        const uint4 all = *reinterpret_cast<const uint4*>(tops);
+        const uint32_t ex = max(1u, max(max(all.x, all.y), max(all.z, all.w)) >> 23);
         const float down = __uint_as_float(ex == 254 ? 0x00400000u : (254 - ex) << 23);
-        if (i == 0) *reinterpret_cast<uint32_t*>(smem + F::SC + (kv & 3) * F::SC_STAGE + 16) = ex << 23;
+        if (i == 0) *reinterpret_cast<uint32_t*>(scp + 16) = ex << 23;
         mbar_arrive(&bars->sc[kv & 3]);
-        auto store = [&](uint8_t* tile, const uint4 (&x)[CH], bool value) {
+        uint32_t k_hi, k_lo, v_hi, v_lo;
+        {
+          const float sc = v_fine ? ksc * down : __uint_as_float(0x7fc00000u);
+          const __half hi = __float2half_rn(sc), lo = __float2half_rn(sc - __half2float(hi));
+          k_hi = uint32_t(__half_as_ushort(hi)) * 0x10001u;
+          k_lo = uint32_t(__half_as_ushort(lo)) * 0x10001u;
+          const float vz = v_fine ? vsc : 0.0f, vh = __bfloat162float(__float2bfloat16_rn(vz));
+          v_hi = f32_to_bf16x2(vh, vh);
+          v_lo = f32_to_bf16x2(vz - vh, vz - vh);
+        }
+        auto store = [&](uint8_t* tile, const uint4 (&x)[CH], bool value, uint32_t s_hi, uint32_t s_lo) {
+          uint8_t* row = tile + i * 128;
+          const int turn = i & 7;
 #pragma unroll
           for (int k = 0; k < CH; ++k) {
-            const int tk = i / CH + (128 / CH) * k;
-            uint32_t s_hi, s_lo;
-            if (value) {
-              const float sc = reinterpret_cast<const float*>(tsp)[128 + tk];
-              const float hi = __bfloat162float(__float2bfloat16_rn(sc));
-              s_hi = f32_to_bf16x2(hi, hi);
-              s_lo = f32_to_bf16x2(sc - hi, sc - hi);
-            } else {
-              const float sc = reinterpret_cast<const float*>(tsp)[tk] * down;
-              const __half hi = __float2half_rn(sc), lo = __float2half_rn(sc - __half2float(hi));
-              s_hi = uint32_t(__half_as_ushort(hi)) * 0x10001u;
-              s_lo = uint32_t(__half_as_ushort(lo)) * 0x10001u;
-            }
             const uint32_t wd[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
             constexpr int OUT = 128 / (8 * BITS);  // 16-byte chunks of operand from 16 bytes of codes
-            const int c0 = OUT * piece;
-            uint8_t* row = tile + (c0 / 8) * 16384 + tk * 128;
-            // lanes of different column blocks store their chunks in another order (bank conflicts)
-            const int turn = D == 128 ? (BITS == 4 ? 2 * (c0 / 8) : c0 / 8) : 0;
 #pragma unroll
-            for (int e0 = 0; e0 < OUT; ++e0) {
+            for (int e = 0; e < OUT; ++e) {
               uint32_t o[4];
-              const int e = e0 ^ turn;
               if constexpr (BITS == 4) {
-                const uint32_t u = e == 0 ? wd[0] : e == 1 ? wd[1] : e == 2 ? wd[2] : wd[3];
-                if (value) bf_of4(u, o);
-                else half_of4(u, o);
+                if (value) bf_of4(wd[e], o);
+                else half_of4(wd[e], o);
               } else {
-                const uint32_t u0 = e == 0 ? wd[0] : wd[2], u1 = e == 0 ? wd[1] : wd[3];
                 if (value) {
-                  bf_of8(u0, o[0], o[1]);
-                  bf_of8(u1, o[2], o[3]);
+                  bf_of8(wd[2 * e], o[0], o[1]);
+                  bf_of8(wd[2 * e + 1], o[2], o[3]);
                 } else {
-                  half_of8(u0, o[0], o[1]);
-                  half_of8(u1, o[2], o[3]);
+                  half_of8(wd[2 * e], o[0], o[1]);
+                  half_of8(wd[2 * e + 1], o[2], o[3]);
                 }
               }
 #pragma unroll
               for (int y = 0; y < 4; ++y)
                 o[y] = value ? bfma2(o[y], s_hi, bfma2(o[y], s_lo, 0x80008000u)) : hfma2(o[y], s_hi, hfma2(o[y], s_lo, 0x80008000u));
-              *reinterpret_cast<uint4*>(row + (((c0 % 8) + e) ^ (tk & 7)) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+              const int c = OUT * k + e;  // chunk of the position's row
+              *reinterpret_cast<uint4*>(row + (c / 8) * 16384 + ((c % 8) ^ turn) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
             }
           }
         };
-        store(smem + F::K + st * F::TILE, kr, false);
+        store(smem + F::K + st * F::TILE, kr, false, k_hi, k_lo);
         fence_proxy_async_smem();
         mbar_arrive(&bars->kfull[st]);
         // the next unit's codes are on their way while this one's are waited for and unpacked
-        if (j + 1 < g.ue) {
-          find(j + 1);
-          load(a.k_codes, kr);
-          load_scales();
-        }
+        vec = vector_of(j + 1, page);
+        load_scales(vec);
+        load(a.k_codes, vec, kr);
         ok = round == 0 || mbar_wait(&bars->vempty[st], (round - 1) & 1u);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        store(smem + F::V + st * F::TILE, vr, true);
+        store(smem + F::V + st * F::TILE, vr, true, v_hi, v_lo);
         fence_proxy_async_smem();
         mbar_arrive(&bars->vfull[st]);
-        if (j + 1 < g.ue) load(a.v_codes, vr);
+        load(a.v_codes, vec, vr);
       }
     }
-    if (!ok && !*abort) give_up();
+    if ((!ok || more < 0) && !*abort) give_up();
   } else {
-    regs_less<48>();
+    regs_less<80>();
     if (warp == 12) {
       // ---------------- products: the warp waits, one thread issues ----------------
-      w.start(bars);
       constexpr uint32_t id_s = instr_desc(false, 128, false), id_o = instr_desc(true, D, true);
       const uint32_t base = smem_u32(smem);
       // descriptors of the tiles: the upper word is the same for all, the lower one holds the address
@@ -866,17 +925,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
       uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
       uint32_t kv0 = 0;
       bool ok = true;
-      for (bool more = w.begin(a, t); more && ok; more = w.next(a, t)) {
-        const Segment& g = w.g;
-        for (int j = g.ub - 1; j < g.ue && ok; ++j) {
-          if (g.ub == g.ue) break;
-          const uint32_t kv = kv0 + uint32_t(j - g.ub);  // unit j (j = ub - 1: none)
+      while (ok && (more = w.next(lane)) > 0) {
+        const int ub = w.seg().ub, ue = w.seg().ue;
+        const int js[2] = {w.seg().half[0].js, w.seg().half[1].js}, je[2] = {w.seg().half[0].je, w.seg().half[1].je};
+        for (int j = ub - 1; j < ue && ok && ub < ue; ++j) {
+          const uint32_t kv = kv0 + uint32_t(j - ub);  // unit j (j = ub - 1: none)
           const uint32_t kn = kv + 1;
           bool have_v = false, have_k = false;
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            const Half& f = g.half[hf];
-            if (ok && j >= f.js && j < f.je) {
+            if (ok && j >= js[hf] && j < je[hf]) {
               if (!have_v) ok = mbar_wait(&bars->vfull[kv & 1], (kv >> 1) & 1u);
               have_v = true;
               ok = ok && !*abort && mbar_wait(&bars->p[hf], np[hf] & 1u);
@@ -886,17 +944,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
               fence_after();
               if (elect_one()) {
                 const uint32_t lo = v_lo + (kv & 1) * (F::TILE >> 4);
-                const bool add = j > f.js;
+                const bool add = j > js[hf];
 #pragma unroll
                 for (int k = 0; k < kKeys / 16; ++k)
                   mma_ts(tmem + F::O_COL + D * hf, tmem + F::S_COL + 128 * hf + 8 * k, lo + k * 128, v_hi, id_o, k > 0 || add);
                 commit(&bars->o[hf]);
               }
             }
-            if (ok && j + 1 >= f.js && j + 1 < f.je) {
+            if (ok && j + 1 >= js[hf] && j + 1 < je[hf]) {
               if (!have_k) ok = mbar_wait(&bars->kfull[kn & 1], (kn >> 1) & 1u);
               have_k = true;
-              if (ok && j + 1 == f.js) ok = mbar_wait(&bars->q[hf], nq[hf]++ & 1u);
+              if (ok && j + 1 == js[hf]) ok = mbar_wait(&bars->q[hf], nq[hf]++ & 1u);
               ok = __all_sync(0xffffffffu, ok && !*abort);
               if (!ok) break;
               fence_after();
@@ -913,17 +971,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
           }
           if (!ok) break;
           if (elect_one()) {
-            if (j >= g.ub) commit(&bars->vempty[kv & 1]);
-            if (j + 1 < g.ue) commit(&bars->kempty[kn & 1]);
+            if (j >= ub) commit(&bars->vempty[kv & 1]);
+            if (j + 1 < ue) commit(&bars->kempty[kn & 1]);
           }
           __syncwarp();
         }
-        kv0 += uint32_t(g.ue - g.ub);
+        kv0 += uint32_t(ue - ub);
       }
-      if (!ok && !*abort) give_up();
+      if ((!ok || more < 0) && !*abort) give_up();
       // every product has ended before tensor memory is given back
       if (elect_one()) commit(&bars->done);
       if (!mbar_wait(&bars->done, 0u)) atomicAdd(&g_wait_timeouts_kv, 1u);
+    } else if (warp == 13 && lane == 0) {
+      if (!walk(a, t, bars, &ring, abort)) give_up();
     }
   }
   __syncwarp();
