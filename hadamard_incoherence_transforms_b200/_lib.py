@@ -42,7 +42,7 @@ SIGNATURES = {
     "qwha_select": (_i32, [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp]),
     "harp_blocks": (_i32, [_vp, _vp, ctypes.c_float, _i64, _i32, _vp, _vp, _vp, _vp]),
     "rht_kv_append": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _i32, _vp]),
-    "rht_kv_workspace_bytes": (_sz, [_i32, _i32, _i32]),
+    "rht_kv_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32, _i64]),
     "rht_kv_attention": (_i32, [_vp, _vp, _vp, _i64, _i32, _i64, _i64, _i64, _i64, _i32, _i32, ctypes.c_float, _i32,
                                 _i64, _i64, _vp, _sz, _vp]),
     "rht_kv_read": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _i32, _vp]),

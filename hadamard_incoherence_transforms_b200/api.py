@@ -530,14 +530,15 @@ def rht_kv_attention(q, k_codes, k_scales, v_codes, v_scales, page_table, lens, 
             raise ValueError("out must have q's shape and device")
     kv = _kv(d, dev, n, k_codes, k_scales, v_codes, v_scales, page_table, lens, cu, k_signs, v_signs, inv_freq,
              interleaved, positions, rope_axis)
-    need = load().rht_kv_workspace_bytes(heads, k_codes.shape[1], d)
+    max_new = max(n, 1) if max_new is None else int(max_new)
+    need = load().rht_kv_workspace_bytes(n, heads, k_codes.shape[1], d, max_new)
     ws = workspace
     if ws is None and need > 0:
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
     _kv_call(dev, "rht_kv_attention", kv, q.data_ptr(), out.data_ptr(), n, heads, q.stride(0), q.stride(1),
              out.stride(0), out.stride(1), _dt(q.dtype), _dt(out.dtype),
              float(d ** -0.5 if sm_scale is None else sm_scale), int(bool(causal)), int(window),
-             int(max(n, 1) if max_new is None else max_new), _ptr(ws),
+             max_new, _ptr(ws),
              0 if ws is None else ws.numel() * ws.element_size())
     return out
 

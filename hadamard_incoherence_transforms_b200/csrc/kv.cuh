@@ -211,61 +211,4 @@ __device__ __forceinline__ void kv_rope(float (&x)[32], const void* p, int64_t a
   }
 }
 
-// The same turn with the angles found on the way (positions and queries of
-// long calls, where a table of them would not fit).  OWN: every pair turns by the
-// token's own position.
-template <int D, bool F32, bool OWN>
-__device__ __forceinline__ void kv_rope_pairs(float (&x)[32], const void* src, int64_t at, const KvArgs& a,
-                                              const uint64_t* turns, int64_t t, int pos, int l) {
-  constexpr int LPV = KvLanes<D>::LPV;
-  auto angle = [&](int j) {
-    const float h = kv_halfturns(OWN ? pos : kv_turn_pos(a, t, pos, j), turns[j]) * 3.14159265358979f;
-    return make_float2(__cosf(h), __sinf(h));
-  };
-  if (a.interleaved) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int i0 = 8 * (c * LPV + l);
-      if (i0 >= 2 * a.n_freq) continue;
-#pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        const float2 cs = angle((i0 + e) / 2);
-        const float u = x[8 * c + e], w = x[8 * c + e + 1];
-        x[8 * c + e] = u * cs.x - w * cs.y;
-        x[8 * c + e + 1] = u * cs.y + w * cs.x;
-      }
-    }
-  } else if (2 * a.n_freq == D) {  // both chunks of a pair are the lane's own
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float2 cs = angle(8 * ((i / 8) * LPV + l) + i % 8);
-      const float u = x[i], w = x[i + 16];
-      x[i] = u * cs.x - w * cs.y;
-      x[i + 16] = u * cs.y + w * cs.x;
-    }
-  } else {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int i0 = 8 * (c * LPV + l);
-      if (i0 >= 2 * a.n_freq) continue;
-      const bool low = i0 < a.n_freq;
-      float o[8];
-      kv_load8<F32>(src, at + (low ? i0 + a.n_freq : i0 - a.n_freq), o);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float2 cs = angle((low ? i0 : i0 - a.n_freq) + e);
-        float& v = x[8 * c + e];
-        v = low ? v * cs.x - o[e] * cs.y : o[e] * cs.y + v * cs.x;
-      }
-    }
-  }
-}
-template <int D, bool F32>
-__device__ __forceinline__ void kv_rope_direct(float (&x)[32], const void* src, int64_t at, const KvArgs& a,
-                                               const uint64_t* turns, int64_t t, int pos, int l) {
-  if (a.n_freq == 0) return;
-  if (a.positions == nullptr) kv_rope_pairs<D, F32, true>(x, src, at, a, turns, t, pos, l);
-  else kv_rope_pairs<D, F32, false>(x, src, at, a, turns, t, pos, l);
-}
-
 }  // namespace hit

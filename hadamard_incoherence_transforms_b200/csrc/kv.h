@@ -50,7 +50,8 @@ struct KvAttn {
 };
 size_t kv_few_bytes(int head_dim);  // workspace
 cudaError_t launch_kv_few(const KvArgs& a, const KvAttn& t, cudaStream_t st);
-size_t kv_prompt_bytes(int head_dim);
+size_t kv_prompt_bytes(int64_t tokens, int heads, int head_dim);
+cudaError_t launch_kv_prompt_queries(const KvArgs& a, const KvAttn& t, cudaStream_t st);
 cudaError_t launch_kv_prompt(const KvArgs& a, const KvAttn& t, cudaStream_t st);
 cudaError_t wait_timeouts_kv(unsigned long long* count, bool reset);
 

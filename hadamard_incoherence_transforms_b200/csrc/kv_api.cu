@@ -31,6 +31,12 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 constexpr int64_t kMaxTokens = int64_t(1) << 31;
 constexpr int64_t kFewRows = 16;
 
+// Sequences with up to kFewRows query rows for a key/value head go to the kernel
+// that streams the codes once for 16 rows, the others to the one that works on
+// 256 rows at a time.  Each launch leaves the other's sequences alone, so that
+// max_new decides only whether the second kind is needed.
+bool few_only(int64_t max_new, int64_t group, int head_dim) { return head_dim == 256 || max_new * group <= kFewRows; }
+
 // Checks what the three calls share and fills `a`.  `rope`: whether the call
 // uses the rotary fields.
 int check_kv(const char* fn, const hit_kv* c, int64_t tokens, bool rope, hit::KvArgs& a) {
@@ -156,9 +162,13 @@ int rht_kv_read(const hit_kv* kv, void* k, void* v, int64_t rows, int64_t k_ts, 
   return cuda_status(hit::launch_kv_read(a, y, dtype, static_cast<cudaStream_t>(stream)), fn);
 }
 
-size_t rht_kv_workspace_bytes(int heads, int kv_heads, int head_dim) {
-  if (heads < 1 || kv_heads < 1 || (head_dim != 64 && head_dim != 128 && head_dim != 256)) return 0;
-  return std::max(hit::kv_few_bytes(head_dim), hit::kv_prompt_bytes(head_dim));
+size_t rht_kv_workspace_bytes(int64_t tokens, int heads, int kv_heads, int head_dim, int64_t max_new) {
+  if (tokens < 1 || tokens >= kMaxTokens || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 || max_new < 1 ||
+      (head_dim != 64 && head_dim != 128 && head_dim != 256))
+    return 0;
+  const size_t few = hit::kv_few_bytes(head_dim);
+  if (few_only(std::min(tokens, max_new), heads / kv_heads, head_dim)) return few;
+  return std::max(few, hit::kv_prompt_bytes(tokens, heads, head_dim));
 }
 
 int rht_kv_attention(const hit_kv* kv, const void* q, void* out, int64_t tokens, int heads, int64_t q_ts, int64_t q_hs,
@@ -181,7 +191,7 @@ int rht_kv_attention(const hit_kv* kv, const void* q, void* out, int64_t tokens,
   if (r) return r;
   r = check_dense(fn, "out", out, o_ts, o_hs, dtype_out);
   if (r) return r;
-  const size_t need = rht_kv_workspace_bytes(heads, a.hk, a.head_dim);
+  const size_t need = rht_kv_workspace_bytes(tokens, heads, a.hk, a.head_dim, max_new);
   if (need > 0) {
     if (workspace == nullptr || workspace_bytes < need)
       return fail(HIT_EWORKSPACE, "%s: needs %zu workspace bytes", fn, need);
@@ -204,15 +214,12 @@ int rht_kv_attention(const hit_kv* kv, const void* q, void* out, int64_t tokens,
   t.max_new = max_new < tokens ? max_new : tokens;
   t.ws = workspace;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // Sequences with up to kFewRows query rows for a key/value head go to the kernel
-  // that streams the codes once for 16 rows, the others to the one that works
-  // on 256 rows at a time; each launch leaves the other's sequences alone, so
-  // that max_new decides only whether the second launch is needed.
-  if (a.head_dim == 256 || t.max_new * t.group <= kFewRows) return cuda_status(hit::launch_kv_few(a, t, st), fn);
+  if (few_only(t.max_new, t.group, a.head_dim)) return cuda_status(hit::launch_kv_few(a, t, st), fn);
   hit::KvAttn few = t;
   few.rows_hi = few.max_new = kFewRows;
   t.rows_lo = kFewRows + 1;
-  r = cuda_status(hit::launch_kv_few(a, few, st), fn);
+  r = cuda_status(hit::launch_kv_prompt_queries(a, t, st), fn);
+  if (r == HIT_OK) r = cuda_status(hit::launch_kv_few(a, few, st), fn);
   return r ? r : cuda_status(hit::launch_kv_prompt(a, t, st), fn);
 }
 

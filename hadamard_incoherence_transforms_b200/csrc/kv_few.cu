@@ -523,7 +523,7 @@ cudaError_t go(const KvArgs& a, const KvAttn& t, cudaStream_t st) {
   kernel<<<ctas, kThreads, bytes, st>>>(a, t);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_kv_join<D, 8 * NT>(a, t, ctas, st);
+  return launch_kv_join<D, 8 * NT, 8 * NT>(a, t, ctas, st);
 }
 
 }  // namespace

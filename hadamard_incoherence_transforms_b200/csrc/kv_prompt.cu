@@ -43,8 +43,7 @@ struct Prompt {
   static constexpr int Q = 0, K = 2 * TILE, V = 4 * TILE, SC = 6 * TILE;
   // ring of four units: which positions exist (128 bits), the power of two of the key scales
   static constexpr int SC_STAGE = 32;
-  static constexpr int ES = SC + 4 * SC_STAGE;   // 256 row factors
-  static constexpr int TS = ES + kRows * 4;      // the largest key scale of each unpacking warp, two units
+  static constexpr int TS = SC + 4 * SC_STAGE;   // the largest key scale of each unpacking warp, two units
   static constexpr int BARS = TS + 32;
   static constexpr int BYTES = BARS + 512 + 1024;
   static constexpr int S_COL = 0, O_COL = 2 * 128;  // tensor memory columns
@@ -525,6 +524,97 @@ __host__ __device__ constexpr int v_elem(int c) {
   return BITS == 4 ? (c >> 1) + 4 * (c & 1) : (c & 4) + 2 * (c & 1) + ((c >> 1) & 1);
 }
 
+// ---------------------------------------------------------------------------
+// Queries of the sequences that belong to the launch: turned, rotated, scaled
+// into base-2 scores, each row brought to [-2, 2) by its power of two and rounded
+// to fp16, in the order of the keys' elements.  A launch of its own: done inside
+// the attention kernel, whose warps then had nothing else to do, it took 30,000
+// cycles for every 256 rows.
+// ---------------------------------------------------------------------------
+constexpr int kQueryTile = 8;  // tokens
+template <int D>
+struct QueryWork {
+  __half* rows;    // [tokens, heads, D]
+  float* factors;  // [tokens, heads]
+};
+template <int D>
+__host__ __device__ __forceinline__ QueryWork<D> query_work_of(void* ws, int64_t tokens, int heads) {
+  uint8_t* p = static_cast<uint8_t*>(ws) + kv_work_bytes<D, kRows>(kCtas);
+  QueryWork<D> w;
+  w.rows = reinterpret_cast<__half*>(p);
+  w.factors = reinterpret_cast<float*>(p + size_t(tokens) * heads * D * 2);
+  return w;
+}
+
+template <int D, int BITS>
+__global__ void __launch_bounds__(256) k_kv_query(const KvArgs a, const KvAttn t) {
+  constexpr int LPV = KvLanes<D>::LPV;
+  __shared__ float2 cs[kQueryTile * (D / 2)];
+  __shared__ uint64_t turns[D / 2];
+  __shared__ int pos[kQueryTile], mine[kQueryTile];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t0 = int64_t(blockIdx.x) * kQueryTile;
+  const int nt = int(min(int64_t(kQueryTile), a.tokens - t0));
+  if (warp < nt) {
+    const KvToken k = kv_token(a, t0 + warp, lane);
+    if (lane == 0) {
+      pos[warp] = int(k.pos);
+      const int64_t rows = k.seq < 0 ? 0 : (min(int64_t(a.cu[k.seq + 1]), a.tokens) - a.cu[k.seq]) * t.group;
+      mine[warp] = k.seq >= 0 && rows >= t.rows_lo && rows <= t.rows_hi;
+    }
+  }
+  kv_turns(a, turns, threadIdx.x, blockDim.x);
+  __syncthreads();
+  for (int i = threadIdx.x; i < nt * a.n_freq; i += blockDim.x) {
+    const int j = i / a.n_freq, f = i - j * a.n_freq;
+    if (mine[j]) cs[i] = kv_angle_fast(a, turns, t0 + j, pos[j], f);
+  }
+  __syncthreads();
+  const QueryWork<D> w = query_work_of<D>(t.ws, a.tokens, t.heads);
+  const int l = threadIdx.x % LPV;
+  const int vectors = nt * t.heads, per = blockDim.x / LPV;
+  for (int v0 = blockIdx.y * per; v0 < vectors; v0 += gridDim.y * per) {
+    const int v = v0 + int(threadIdx.x) / LPV;
+    const int j = v < vectors ? v / t.heads : 0, head = v - j * t.heads;
+    const bool live = v < vectors && mine[j];
+    if (!__any_sync(0xffffffffu, live)) continue;
+    float x[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = 0.0f;
+    if (live) {
+      const int64_t at = (t0 + j) * t.q_ts + head * t.q_hs;
+      if (t.q_f32) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) kv_load8<true>(t.q, at + 8 * (c * LPV + l), x + 8 * c);
+        if (a.n_freq > 0) kv_rope<D, true>(x, t.q, at, cs + j * a.n_freq, a.n_freq, a.interleaved, l);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) kv_load8<false>(t.q, at + 8 * (c * LPV + l), x + 8 * c);
+        if (a.n_freq > 0) kv_rope<D, false>(x, t.q, at, cs + j * a.n_freq, a.n_freq, a.interleaved, l);
+      }
+      kv_signs<D>(x, a.k_signs, l);
+    }
+    kv_hadamard<D>(x, l);
+    float up, down;
+    kv_query_scale<D>(x, t.scale, up, down);
+    if (live) {
+      const int64_t row = (t0 + j) * t.heads + head;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i0 = BITS == 4 ? e : 2 * e, i1 = BITS == 4 ? e + 4 : 2 * e + 1;
+          const __half2 p = __floats2half2_rn(x[8 * c + i0] * down, x[8 * c + i1] * down);
+          y[e] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+        *reinterpret_cast<uint4*>(w.rows + row * D + 8 * (c * LPV + l)) = make_uint4(y[0], y[1], y[2], y[3]);
+      }
+      if (l == 0) w.factors[row] = up;
+    }
+  }
+}
+
 template <int D, int BITS>
 __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const KvAttn t) {
   using F = Prompt<D>;
@@ -562,14 +652,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  __shared__ uint64_t turns[D / 2];
-  __shared__ uint32_t k_neg[D / 32], v_neg[D / 32];  // a bit for each element whose sign is flipped
-  kv_turns(a, turns, threadIdx.x, kThreads);
+  __shared__ uint32_t v_neg[D / 32];  // a bit for each element of the result whose sign is flipped
   if (warp >= 4 && warp < 4 + D / 32) {
-    const int i = 32 * (warp - 4) + lane;
-    const uint32_t kb = __ballot_sync(0xffffffffu, a.k_signs != nullptr && __ldg(a.k_signs + i) < 0);
-    const uint32_t vb = __ballot_sync(0xffffffffu, a.v_signs != nullptr && __ldg(a.v_signs + i) < 0);
-    if (lane == 0) k_neg[warp - 4] = kb, v_neg[warp - 4] = vb;
+    const uint32_t b = __ballot_sync(0xffffffffu, a.v_signs != nullptr && __ldg(a.v_signs + 32 * (warp - 4) + lane) < 0);
+    if (lane == 0) v_neg[warp - 4] = b;
   }
   if (warp == 0) plan_warp(a, t, bars, lane);
   fence_before();
@@ -585,11 +671,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
   int more = 1;
   if (warp < 8) {
     regs_more<160>();
+    // the launch begins before the one ahead of it has ended: the queries, and
+    // the workspace that is written here, are its
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     // ---------------- softmax of half `hf`, a thread a row ----------------
     const int hf = warp >> 2, r = threadIdx.x & 127;
     const uint32_t lane_at = tmem + (uint32_t(32 * (warp & 3)) << 16);
     const uint32_t s_at = lane_at + F::S_COL + 128 * hf, o_at = lane_at + F::O_COL + D * hf;
-    float* es = reinterpret_cast<float*>(smem + F::ES) + 128 * hf;
+    const QueryWork<D> queries = query_work_of<D>(t.ws, a.tokens, t.heads);
     const KvWork work = kv_work_of<D, kRows>(t.ws, gridDim.x);
     uint32_t ns = 0, no = 0;  // score units and outputs seen so far
     uint32_t kv0 = 0;         // units converted before this segment
@@ -605,58 +694,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
       float m = -INFINITY, l = 0.0f;
       bool ok = true;
       if (f.js < f.je) {
-        // the half's queries: turned, rotated, scaled into base-2 scores, brought to [-2, 2)
-        constexpr int LPV = KvLanes<D>::LPV;
-        const int ln = r % LPV;
-#pragma unroll 1
-        for (int q0 = 0; q0 < 128; q0 += 128 / LPV) {
-          const int qr = q0 + r / LPV;
-          float x[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = 0.0f;
-          if (qr < f.rows) {
-            const int row_q = g.row0 + 128 * hf + qr, tk = row_q / t.group;
-            const int64_t src = (g.t0 + tk) * t.q_ts + (int64_t(g.h) * t.group + row_q - tk * t.group) * t.q_hs;
-            if (t.q_f32) {
-#pragma unroll
-              for (int c = 0; c < 4; ++c) kv_load8<true>(t.q, src + 8 * (c * LPV + ln), x + 8 * c);
-              if (a.n_freq > 0) kv_rope_direct<D, true>(x, t.q, src, a, turns, g.t0 + tk, int(g.pos0) + tk, ln);
-            } else {
-#pragma unroll
-              for (int c = 0; c < 4; ++c) kv_load8<false>(t.q, src + 8 * (c * LPV + ln), x + 8 * c);
-              if (a.n_freq > 0) kv_rope_direct<D, false>(x, t.q, src, a, turns, g.t0 + tk, int(g.pos0) + tk, ln);
-            }
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int ch = c * LPV + ln;
-              const uint32_t neg = k_neg[ch >> 2] >> (8 * (ch & 3));
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                x[8 * c + e] = __uint_as_float(__float_as_uint(x[8 * c + e]) ^ ((neg << (31 - e)) & 0x80000000u));
-            }
-          }
-          kv_hadamard<D>(x, ln);
-          float up, down;
-          kv_query_scale<D>(x, t.scale, up, down);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int d0 = 8 * (c * LPV + ln);
-            uint32_t v[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int i = BITS == 4 ? e : 2 * e, j = BITS == 4 ? e + 4 : 2 * e + 1;
-              const __half2 p = __floats2half2_rn(x[8 * c + i] * down, x[8 * c + j] * down);
-              v[e] = *reinterpret_cast<const uint32_t*>(&p);
-            }
-            *reinterpret_cast<uint4*>(smem + F::Q + hf * F::TILE + (d0 / 64) * 16384 + qr * 128 +
-                                      (((d0 % 64) / 8) ^ (qr & 7)) * 16) = make_uint4(v[0], v[1], v[2], v[3]);
-          }
-          if (ln == 0) es[qr] = up;
+        // the half's queries, a row's 16-byte pieces to their swizzled places
+        constexpr int PIECES = D / 8;
+#pragma unroll 4
+        for (int k = 0; k < PIECES; ++k) {
+          const int qr = (k * 128 + r) / PIECES, c = r % PIECES;
+          const int row_q = g.row0 + 128 * hf + qr, tk = row_q / t.group;
+          const bool there = qr < f.rows;
+          const int64_t src = there ? (g.t0 + tk) * t.heads + g.h * t.group + (row_q - tk * t.group) : 0;
+          const uint32_t dst = smem_u32(smem) + F::Q + hf * F::TILE + (c / 8) * 16384 + qr * 128 + ((c % 8) ^ (qr & 7)) * 16;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(queries.rows + src * D + 8 * c),
+                       "r"(there ? 16 : 0)
+                       : "memory");
         }
+        const float qe = mine ? queries.factors[(g.t0 + tok) * t.heads + head] : 1.0f;
+        asm volatile("cp.async.wait_all;" ::: "memory");
         fence_proxy_async_smem();
         mbar_arrive(&bars->q[hf]);
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + hf) : "memory");
-        const float qe = es[r];
         const int64_t pos = g.pos0 + tok;
         const int64_t hi = mine ? (t.causal ? min(g.hi, pos + 1) : g.hi) : 0;
         const int64_t lo = t.window > 0 ? pos - t.window + 1 : 0;
@@ -996,6 +1050,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
 }
 
 template <int D, int BITS>
+cudaError_t prepare(const KvArgs& a, const KvAttn& t, cudaStream_t st) {
+  const int64_t tiles = (a.tokens + kQueryTile - 1) / kQueryTile;
+  const int64_t passes = (int64_t(kQueryTile) * t.heads * (D / 32) + 255) / 256;
+  // heads are dealt to several CTAs while the tokens alone do not fill the GPU four times
+  const unsigned y = unsigned(std::max<int64_t>(1, std::min(passes, 4 * 148 * 4 / tiles)));
+  k_kv_query<D, BITS><<<dim3(unsigned(tiles), y), 256, 0, st>>>(a, t);
+  return cudaGetLastError();
+}
+
+template <int D, int BITS>
 cudaError_t go(const KvArgs& a, const KvAttn& t, cudaStream_t st) {
   constexpr int bytes = Prompt<D>::BYTES;
   auto* kernel = k_kv_prompt<D, BITS>;
@@ -1009,18 +1073,33 @@ cudaError_t go(const KvArgs& a, const KvAttn& t, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit);
   }
-  kernel<<<kCtas, kThreads, bytes, st>>>(a, t);
-  e = cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kCtas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kernel, a, t);
   if (e != cudaSuccess) return e;
-  return launch_kv_join<D, kRows>(a, t, kCtas, st);
+  return launch_kv_join<D, kRows, 32>(a, t, kCtas, st);
 }
 
 }  // namespace
 
-size_t kv_prompt_bytes(int head_dim) {
-  return head_dim == 64 ? kv_work_bytes<64, kRows>(kCtas) : head_dim == 128 ? kv_work_bytes<128, kRows>(kCtas) : 0;
+size_t kv_prompt_bytes(int64_t tokens, int heads, int head_dim) {
+  const size_t queries = size_t(tokens) * heads * (size_t(head_dim) * 2 + 4);
+  return (head_dim == 64 ? kv_work_bytes<64, kRows>(kCtas) : kv_work_bytes<128, kRows>(kCtas)) + queries;
 }
 
+// Two launches; nothing else may write the workspace's part for queries between them.
+cudaError_t launch_kv_prompt_queries(const KvArgs& a, const KvAttn& t, cudaStream_t st) {
+  if (a.head_dim == 64) return a.bits == 4 ? prepare<64, 4>(a, t, st) : prepare<64, 8>(a, t, st);
+  return a.bits == 4 ? prepare<128, 4>(a, t, st) : prepare<128, 8>(a, t, st);
+}
 cudaError_t launch_kv_prompt(const KvArgs& a, const KvAttn& t, cudaStream_t st) {
   if (a.head_dim == 64) return a.bits == 4 ? go<64, 4>(a, t, st) : go<64, 8>(a, t, st);
   return a.bits == 4 ? go<128, 4>(a, t, st) : go<128, 8>(a, t, st);

@@ -196,30 +196,32 @@ __device__ __forceinline__ float kv_max(float a, float b) {
 }
 
 // Joins the parts of the pairs that several CTAs share: block c handles the
-// pair that CTA c began and did not end (slot 2 c + 1).  A row's parts are
-// dealt to the warps left over by the number of rows.
+// pair that CTA c began and did not end (slot 2 c + 1), rows PER y ... of it.  A
+// row's parts are dealt to the warps left over by the number of rows.
 constexpr int kJoinWarps = 16;
-template <int D, int ROWS>
+template <int D, int ROWS, int PER>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_kv_join(const KvArgs a, const KvAttn t, int ctas) {
   constexpr int E = D / 32;
   __shared__ float sx[kJoinWarps][D];
   __shared__ float sm[kJoinWarps], sl[kJoinWarps];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const KvWork w = kv_work_of<D, ROWS>(t.ws, ctas);
-  const int c = blockIdx.x;
+  const int c = blockIdx.x, first_row = blockIdx.y * PER;
   const KvPart p = w.part[2 * c + 1];
-  if (p.first < 0) return;
+  if (p.first < 0 || first_row >= p.rows) return;
+  const int rows = min(PER, p.rows - first_row);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int per = 1;  // rows handled at once, a power of two
-  while (per < kJoinWarps && per < p.rows) per *= 2;
+  while (per < kJoinWarps && per < rows) per *= 2;
   const int teams = kJoinWarps / per, team = warp / per;
   const int parts = p.last - p.first + 1;
-  for (int r0 = 0; r0 < p.rows; r0 += per) {
-    const int r = r0 + warp % per;
+  for (int r0 = 0; r0 < rows; r0 += per) {
+    const int in = r0 + warp % per, r = first_row + in;
     float m = -INFINITY, l = 0.0f, x[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) x[e] = 0.0f;
-    if (r < p.rows) {
+    if (in < rows) {
       for (int i = team + lane * teams; i < parts; i += 32 * teams)
         m = kv_max(m, w.ms[size_t(i == 0 ? 2 * c + 1 : 2 * (c + i)) * ROWS + r].x);
 #pragma unroll
@@ -267,7 +269,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_kv_join(const KvArgs a, con
       }
       __syncthreads();
     }
-    if (team == 0 && r < p.rows) {
+    if (team == 0 && in < rows) {
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
       for (int e = 0; e < E; ++e) x[e] *= inv;
@@ -277,10 +279,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_kv_join(const KvArgs a, con
   }
 }
 
-template <int D, int ROWS>
+template <int D, int ROWS, int PER>
 cudaError_t launch_kv_join(const KvArgs& a, const KvAttn& t, int ctas, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(unsigned(ctas));
+  cfg.gridDim = dim3(unsigned(ctas), (ROWS + PER - 1) / PER);
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -288,7 +290,7 @@ cudaError_t launch_kv_join(const KvArgs& a, const KvAttn& t, int ctas, cudaStrea
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_kv_join<D, ROWS>, a, t, ctas);
+  return cudaLaunchKernelEx(&cfg, k_kv_join<D, ROWS, PER>, a, t, ctas);
 }
 
 }  // namespace hit

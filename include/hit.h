@@ -408,10 +408,10 @@ HIT_API int harp_blocks(const float* theta, const int8_t* theta_q, float theta_s
  *   rows (tokens * heads / kv_heads) for a key/value head, or head_dim is 256,
  *   codes and scales enter exactly; in longer chunks keys are rounded once to
  *   fp16 and values once to bf16, as an unquantized cache would hold them.
- *   max_new: an
- *   upper bound of n_s (any value >= 1 is right; a tight one saves a launch).
- *   Needs rht_kv_workspace_bytes(heads, kv_heads, head_dim) bytes of 16-byte
- *   aligned workspace, which calls that may run at the same time must not share.
+ *   max_new: an upper bound of n_s (any value >= 1 gives right results; a tight
+ *   one saves launches and workspace).  Needs rht_kv_workspace_bytes(tokens,
+ *   heads, kv_heads, head_dim, max_new) bytes of 16-byte aligned workspace,
+ *   which calls that may run at the same time must not share.
  * rht_kv_read: k, v [rows, kv_heads, head_dim] <- R^-1 of what the cache
  *   stands for at the call's tokens (rows is the number of tokens; either
  *   output may be NULL).  Keys come back with their rotary turn.
@@ -445,7 +445,7 @@ typedef struct hit_kv {
 
 HIT_API int rht_kv_append(const hit_kv* kv, const void* k, const void* v, int64_t tokens, int64_t k_ts, int64_t k_hs,
                           int64_t v_ts, int64_t v_hs, int dtype, void* stream);
-HIT_API size_t rht_kv_workspace_bytes(int heads, int kv_heads, int head_dim);
+HIT_API size_t rht_kv_workspace_bytes(int64_t tokens, int heads, int kv_heads, int head_dim, int64_t max_new);
 HIT_API int rht_kv_attention(const hit_kv* kv, const void* q, void* out, int64_t tokens, int heads, int64_t q_ts,
                              int64_t q_hs, int64_t o_ts, int64_t o_hs, int dtype_q, int dtype_out, float sm_scale,
                              int causal, int64_t window, int64_t max_new, void* workspace, size_t workspace_bytes,
