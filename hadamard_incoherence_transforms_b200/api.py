@@ -418,9 +418,9 @@ def kv_cache_shapes(pages: int, page_size: int, kv_heads: int, head_dim: int, bi
     return (pages, kv_heads, page_size, head_dim * bits // 8), (pages, kv_heads, page_size)
 
 
-def _kv(d, dev, tokens, k_codes, k_scales, v_codes, v_scales, page_table, lens, cu, k_signs, v_signs, inv_freq=None,
-        interleaved=False, positions=None, rope_axis=None):
-    """The packed struct hit_kv of a call, after checking its tensors against one another."""
+def _kv_refuse(d, dev, tokens, k_codes, k_scales, v_codes, v_scales, page_table, lens, cu, k_signs, v_signs, inv_freq,
+               positions, rope_axis):
+    """Says what is wrong with the tensors of a call."""
     u8, f32, i32 = torch.uint8, torch.float32, torch.int32
     shape = k_codes.shape
     if k_codes.dim() != 4 or k_codes.dtype != u8 or v_codes.dtype != u8 or v_codes.shape != shape:
@@ -429,49 +429,82 @@ def _kv(d, dev, tokens, k_codes, k_scales, v_codes, v_scales, page_table, lens, 
         raise ValueError("k_scales and v_scales must be float32 [pages, kv_heads, page_size]")
     if page_table.dim() != 2 or page_table.dtype != i32 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
         raise ValueError("page_table must be int32 [seqs, pages of a sequence] with unit stride along a row")
-    seqs, max_pages = page_table.shape
+    seqs = page_table.shape[0]
     if lens.dtype != i32 or lens.shape != (seqs,) or cu.dtype != i32 or cu.shape != (seqs + 1,):
         raise ValueError("lens must be int32 [seqs] and cu int32 [seqs + 1]")
-    n_freq, axes, ld_pos = 0, 1, 0
-    tensors = [k_codes, k_scales, v_codes, v_scales, lens, cu]
     for s in (k_signs, v_signs):
-        if s is not None:
-            if s.dtype != torch.int8 or s.shape != (d,):
-                raise ValueError("k_signs and v_signs must be int8 [head_dim]")
-            tensors.append(s)
-    if inv_freq is not None:
-        if inv_freq.dtype != f32 or inv_freq.dim() != 1:
-            raise ValueError("inv_freq must be a float32 vector")
-        tensors.append(inv_freq)
-        n_freq = inv_freq.shape[0]
-        if positions is not None:
-            if positions.dtype != i32 or positions.dim() not in (1, 2) or positions.shape[-1] != tokens:
-                raise ValueError("positions must be int32 [tokens] or [axes, tokens]")
-            tensors.append(positions)
-            axes, ld_pos = (positions.shape[0] if positions.dim() == 2 else 1), tokens
-            if rope_axis is not None:
-                if rope_axis.dtype != torch.int8 or rope_axis.shape != (n_freq,):
-                    raise ValueError("rope_axis must be int8, one axis for each frequency")
-                tensors.append(rope_axis)
-            elif axes != 1:
-                raise ValueError("several position axes need rope_axis")
-        elif rope_axis is not None:
-            raise ValueError("rope_axis needs positions")
-    elif positions is not None or rope_axis is not None:
+        if s is not None and (s.dtype != torch.int8 or s.shape != (d,)):
+            raise ValueError("k_signs and v_signs must be int8 [head_dim]")
+    if inv_freq is None and (positions is not None or rope_axis is not None):
         raise ValueError("positions and rope_axis need inv_freq")
-    for t in tensors:
-        if t.device != dev or not t.is_contiguous():
-            raise ValueError("the cache, lens, cu, signs and positions must be contiguous, all on one CUDA device")
-    if page_table.device != dev:
-        raise ValueError("page_table must be on the cache's device")
-    ptr = [0 if t is None else t.data_ptr()
-           for t in (k_codes, k_scales, v_codes, v_scales, page_table, lens, cu, k_signs, v_signs, inv_freq, positions,
-                     rope_axis)]
-    bits = shape[3] * 8 // d
-    if shape[3] * 8 != d * bits:
+    if inv_freq is not None and (inv_freq.dtype != f32 or inv_freq.dim() != 1):
+        raise ValueError("inv_freq must be a float32 vector")
+    if positions is None and rope_axis is not None:
+        raise ValueError("rope_axis needs positions")
+    if positions is not None:
+        if positions.dtype != i32 or positions.dim() not in (1, 2) or positions.shape[-1] != tokens:
+            raise ValueError("positions must be int32 [tokens] or [axes, tokens]")
+        if rope_axis is None and positions.dim() == 2 and positions.shape[0] != 1:
+            raise ValueError("several position axes need rope_axis")
+        if rope_axis is not None and (rope_axis.dtype != torch.int8 or rope_axis.shape != inv_freq.shape):
+            raise ValueError("rope_axis must be int8, one axis for each frequency")
+    if d < 1 or shape[3] * 8 % d != 0:
         raise ValueError("the codes' last dimension does not fit head_dim")
-    return _KV.pack(*ptr, shape[0], shape[2], page_table.stride(0) if seqs > 1 else max_pages, ld_pos, shape[1], d, bits,
-                    seqs, max_pages, n_freq, axes, int(bool(interleaved)))
+    raise ValueError("the cache, page_table, lens, cu, signs and positions must be on one CUDA device and (but for "
+                     "page_table) contiguous")
+
+
+def _kv(d, dev, tokens, k_codes, k_scales, v_codes, v_scales, page_table, lens, cu, k_signs, v_signs, inv_freq=None,
+        interleaved=False, positions=None, rope_axis=None):
+    """The packed struct hit_kv of a call, after checking its tensors against one another (dev: the device's index, -1
+    for tensors that are on none).  One expression: these checks are a good part of a short call's time."""
+    u8, f32, i32, i8 = torch.uint8, torch.float32, torch.int32, torch.int8
+    shape, three = k_codes.shape, k_scales.shape
+    n_freq, axes, ld_pos, seqs = 0, 1, 0, lens.shape[0] if lens.dim() == 1 else -1
+    fine = (len(shape) == 4 and shape[:3] == three and k_codes.dtype is u8 and v_codes.dtype is u8
+            and k_scales.dtype is f32 and v_scales.dtype is f32 and v_codes.shape == shape and v_scales.shape == three
+            and page_table.dim() == 2 and page_table.dtype is i32 and lens.dtype is i32 and cu.dtype is i32
+            and page_table.shape[0] == seqs and cu.shape == (seqs + 1,)
+            and k_codes.get_device() == dev and k_scales.get_device() == dev and v_codes.get_device() == dev
+            and v_scales.get_device() == dev and page_table.get_device() == dev and lens.get_device() == dev
+            and cu.get_device() == dev and k_codes.is_contiguous() and k_scales.is_contiguous()
+            and v_codes.is_contiguous() and v_scales.is_contiguous() and lens.is_contiguous() and cu.is_contiguous()
+            and (k_signs is None or (k_signs.dtype is i8 and k_signs.shape == (d,) and k_signs.is_contiguous()
+                                     and k_signs.get_device() == dev))
+            and (v_signs is None or (v_signs.dtype is i8 and v_signs.shape == (d,) and v_signs.is_contiguous()
+                                     and v_signs.get_device() == dev)))
+    if fine and inv_freq is not None:
+        fine = (inv_freq.dtype is f32 and inv_freq.dim() == 1 and inv_freq.is_contiguous()
+                and inv_freq.get_device() == dev)
+        n_freq = inv_freq.shape[0] if fine else 0
+        if positions is not None:
+            fine = (fine and positions.dtype is i32 and positions.dim() in (1, 2) and positions.shape[-1] == tokens
+                    and positions.is_contiguous() and positions.get_device() == dev)
+            if fine:
+                axes, ld_pos = (positions.shape[0] if positions.dim() == 2 else 1), tokens
+                fine = axes == 1 if rope_axis is None else (
+                    rope_axis.dtype is i8 and rope_axis.shape == (n_freq,) and rope_axis.is_contiguous()
+                    and rope_axis.get_device() == dev)
+        elif rope_axis is not None:
+            fine = False
+    elif positions is not None or rope_axis is not None:
+        fine = False
+    if fine:
+        max_pages = page_table.shape[1]
+        ld_table, unit = page_table.stride()
+        if seqs < 2:
+            ld_table = max_pages
+        pages, kv_heads, page_size, width = shape
+        fine = (unit == 1 or max_pages < 2) and d > 0 and width * 8 % d == 0
+    if not fine:
+        _kv_refuse(d, dev, tokens, k_codes, k_scales, v_codes, v_scales, page_table, lens, cu, k_signs, v_signs, inv_freq,
+                   positions, rope_axis)
+    return _KV.pack(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
+                    page_table.data_ptr(), lens.data_ptr(), cu.data_ptr(),
+                    0 if k_signs is None else k_signs.data_ptr(), 0 if v_signs is None else v_signs.data_ptr(),
+                    0 if inv_freq is None else inv_freq.data_ptr(), 0 if positions is None else positions.data_ptr(),
+                    0 if rope_axis is None else rope_axis.data_ptr(), pages, page_size, ld_table, ld_pos, kv_heads, d,
+                    width * 8 // d, seqs, max_pages, n_freq, axes, 1 if interleaved else 0)
 
 
 def _kv_dense(t, name, heads=None):
@@ -481,13 +514,21 @@ def _kv_dense(t, name, heads=None):
     return t
 
 
+def _kv_empty(n, heads, d, dtype, device):
+    return torch.empty_strided((n, heads, d), (heads * d, d, 1), dtype=dtype, device=device)
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _kv_call(dev, name, *args):
-    """The call on the tensors' device (it need not be the current one) and its current stream."""
-    if dev.index == torch.cuda.current_device():
-        call(name, *args, torch.cuda.current_stream(dev).cuda_stream)
+    """The call on the tensors' device (an index; it need not be the current one) and its current stream."""
+    if dev == torch.cuda.current_device():
+        call(name, *args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            call(name, *args, torch.cuda.current_stream(dev).cuda_stream)
+            call(name, *args, _raw_stream(dev))
 
 
 def rht_kv_append(k, v, k_codes, k_scales, v_codes, v_scales, page_table, lens, cu, k_signs=None, v_signs=None,
@@ -500,15 +541,16 @@ def rht_kv_append(k, v, k_codes, k_scales, v_codes, v_scales, page_table, lens, 
     positions (int32 [tokens] or [axes, tokens], with rope_axis int8 [n_freq]) replaces the sequence positions."""
     _kv_dense(k, "k")
     _kv_dense(v, "v", k.shape[1])
-    if v.shape != k.shape or v.dtype != k.dtype or v.device != k.device:
+    if v.shape != k.shape or v.dtype != k.dtype or v.get_device() != k.get_device():
         raise ValueError("k and v must have the same shape, dtype and device")
-    if k_codes.shape[1] != k.shape[1]:
+    if k_codes.dim() == 4 and k_codes.shape[1] != k.shape[1]:
         raise ValueError("k's heads are not the cache's")
-    dev, n = k.device, k.shape[0]
-    kv = _kv(k.shape[2], dev, n, k_codes, k_scales, v_codes, v_scales, page_table, lens, cu, k_signs, v_signs, inv_freq,
+    dev, (n, _, d) = k.get_device(), k.shape
+    kv = _kv(d, dev, n, k_codes, k_scales, v_codes, v_scales, page_table, lens, cu, k_signs, v_signs, inv_freq,
              interleaved, positions, rope_axis)
-    _kv_call(dev, "rht_kv_append", kv, k.data_ptr(), v.data_ptr(), n, k.stride(0), k.stride(1), v.stride(0),
-             v.stride(1), _dt(k.dtype))
+    k_ts, k_hs, _ = k.stride()
+    v_ts, v_hs, _ = v.stride()
+    _kv_call(dev, "rht_kv_append", kv, k.data_ptr(), v.data_ptr(), n, k_ts, k_hs, v_ts, v_hs, _dt(k.dtype))
 
 
 def rht_kv_attention(q, k_codes, k_scales, v_codes, v_scales, page_table, lens, cu, k_signs=None, v_signs=None,
@@ -521,25 +563,28 @@ def rht_kv_attention(q, k_codes, k_scales, v_codes, v_scales, page_table, lens, 
     positions up to p (all of them with causal=False; the last `window` ones with window > 0).  max_new bounds the
     tokens of one sequence (default: all of them).  out may be float32 or bfloat16 (default: q's type)."""
     _kv_dense(q, "q")
-    dev, (n, heads, d) = q.device, q.shape
+    dev, (n, heads, d) = q.get_device(), q.shape
     if out is None:
-        out = torch.empty((n, heads, d), dtype=q.dtype, device=dev)
+        out = _kv_empty(n, heads, d, q.dtype, q.device)
     else:
         _kv_dense(out, "out")
-        if out.shape != q.shape or out.device != dev:
+        if out.shape != q.shape or out.get_device() != dev:
             raise ValueError("out must have q's shape and device")
     kv = _kv(d, dev, n, k_codes, k_scales, v_codes, v_scales, page_table, lens, cu, k_signs, v_signs, inv_freq,
              interleaved, positions, rope_axis)
     max_new = max(n, 1) if max_new is None else int(max_new)
-    need = load().rht_kv_workspace_bytes(n, heads, k_codes.shape[1], d, max_new)
-    ws = workspace
-    if ws is None and need > 0:
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    _kv_call(dev, "rht_kv_attention", kv, q.data_ptr(), out.data_ptr(), n, heads, q.stride(0), q.stride(1),
-             out.stride(0), out.stride(1), _dt(q.dtype), _dt(out.dtype),
-             float(d ** -0.5 if sm_scale is None else sm_scale), int(bool(causal)), int(window),
-             max_new, _ptr(ws),
-             0 if ws is None else ws.numel() * ws.element_size())
+    if workspace is None:
+        size = load().rht_kv_workspace_bytes(n, heads, k_codes.shape[1], d, max_new)
+        workspace = torch.empty_strided((size,), (1,), dtype=torch.uint8, device=q.device)
+    else:
+        if _cuda(workspace, "workspace").get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous and on q's device")
+        size = workspace.numel() * workspace.element_size()
+    q_ts, q_hs, _ = q.stride()
+    o_ts, o_hs, _ = out.stride()
+    _kv_call(dev, "rht_kv_attention", kv, q.data_ptr(), out.data_ptr(), n, heads, q_ts, q_hs, o_ts, o_hs, _dt(q.dtype),
+             _dt(out.dtype), float(d ** -0.5 if sm_scale is None else sm_scale), int(bool(causal)), int(window), max_new,
+             workspace.data_ptr(), size)
     return out
 
 
@@ -548,13 +593,19 @@ def rht_kv_read(k_codes, k_scales, v_codes, v_scales, page_table, lens, cu, rows
     """What the cache stands for at the call's tokens: (k, v), each [rows, kv_heads, head_dim], rotated back.
 
     Sequence s owns rows cu[s] .. cu[s + 1], the last of its lens[s] positions; keys keep their rotary turn."""
-    dev = _cuda(k_codes, "k_codes").device
-    shape = (rows, k_codes.shape[1], head_dim)
-    k = torch.empty(shape, dtype=out_dtype, device=dev) if k_out is None else _kv_dense(k_out, "k_out")
-    v = torch.empty(shape, dtype=k.dtype, device=dev) if v_out is None else _kv_dense(v_out, "v_out")
-    if k.shape != shape or v.shape != shape or k.dtype != v.dtype or k.device != dev or v.device != dev:
-        raise ValueError("k_out and v_out must be [rows, kv_heads, head_dim] of one dtype on the cache's device")
+    dev, hk = _cuda(k_codes, "k_codes").get_device(), k_codes.shape[1]
+    if k_out is not None:
+        out_dtype = k_out.dtype
+    elif v_out is not None:
+        out_dtype = v_out.dtype
+    k = _kv_empty(rows, hk, head_dim, out_dtype, k_codes.device) if k_out is None else _kv_dense(k_out, "k_out")
+    v = _kv_empty(rows, hk, head_dim, out_dtype, k_codes.device) if v_out is None else _kv_dense(v_out, "v_out")
+    if k_out is not None or v_out is not None:
+        shape = (rows, hk, head_dim)
+        if k.shape != shape or v.shape != shape or k.dtype != v.dtype or k.get_device() != dev or v.get_device() != dev:
+            raise ValueError("k_out and v_out must be [rows, kv_heads, head_dim] of one dtype on the cache's device")
     kv = _kv(head_dim, dev, rows, k_codes, k_scales, v_codes, v_scales, page_table, lens, cu, k_signs, v_signs)
-    _kv_call(dev, "rht_kv_read", kv, k.data_ptr(), v.data_ptr(), rows, k.stride(0), k.stride(1), v.stride(0),
-             v.stride(1), _dt(k.dtype))
+    k_ts, k_hs, _ = k.stride()
+    v_ts, v_hs, _ = v.stride()
+    _kv_call(dev, "rht_kv_read", kv, k.data_ptr(), v.data_ptr(), rows, k_ts, k_hs, v_ts, v_hs, _dt(out_dtype))
     return k, v
