@@ -31,6 +31,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStages = 3;
+constexpr float kGrow = 65536.0f;
 
 // Positions of a unit: stages of about 4 KB (8 KB for heads of 256), which is
 // 16 warps x 2 stages = 140 KB in flight on an SM.
@@ -59,16 +60,21 @@ __device__ __forceinline__ void mma_b16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
   return r;
 }
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -87,22 +93,26 @@ __device__ __forceinline__ void lds128(uint32_t p, uint32_t* r) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(p));
 }
 
-// Places of 16-byte piece q of position t in a stage.  Score rows r and r + 1
-// are positions that differ in bit 2 (position = r / 2 + 4 (r % 2)), output
-// columns c are positions c, c + 4, ...; the pieces are moved such that the
-// lanes of one shared-memory read touch every bank once.
+// Places of 16-byte piece q of position t in a stage, such that the lanes of one
+// shared-memory read touch every bank once.  Keys are read as 8 positions x 4
+// pieces (16 bytes a lane; 8 bytes where a position has only two pieces), values
+// by 8x8 transposing loads of one piece of 8 positions.
 template <int CH>
 __device__ __forceinline__ int k_place(int t, int q) {
-  if constexpr (CH == 2) return ((t & ~6) | ((t & 2) << 1) | ((t & 4) >> 1)) * CH + q;
-  if constexpr (CH == 4) return (t ^ ((t >> 2) & 1)) * CH + q;
-  return t * CH + (q ^ (t & 4));
+  return CH <= 4 ? t * CH + q : t * CH + (q ^ ((t & 1) << 2));
 }
 template <int CH>
 __device__ __forceinline__ int v_place(int t, int q) {
-  if constexpr (CH == 2) return t * CH + q;
-  if constexpr (CH == 4) return t * CH + (q ^ (t & 2));
-  if constexpr (CH == 8) return t * CH + (q ^ (2 * (t & 3)));
-  return t * CH + (q ^ ((t & 1) | ((t & 2) << 1)));
+  if constexpr (CH == 2) return t * CH + (q ^ ((t >> 2) & 1));
+  if constexpr (CH == 4) return t * CH + (q ^ ((t >> 1) & 3));
+  return t * CH + (q ^ (t & 7));
+}
+// Four 8x8 transposing loads of 16-bit units (`at`: this lane's row of matrix lane / 8).
+__device__ __forceinline__ void load_transposed(uint32_t at, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
 }
 
 template <int D, int BITS, int NT, int MINB>
@@ -110,15 +120,26 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
   using F = Few<D, BITS>;
   constexpr int ROWS = 8 * NT, TK = F::TK, MT = F::MT, CH = F::CH, VB = F::VB, KS = F::KS;
   constexpr int OM = D / 16;   // 16-element tiles of the output's head dimension
-  constexpr int QP = D + 8;    // padded row of the query in shared memory
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint64_t turns[D / 2];
-  kv_turns(a, turns, threadIdx.x, kThreads);  // kv_plan's barriers follow
+  __shared__ uint32_t k_neg[D / 32];  // a bit for each element whose sign is flipped
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r8 = lane >> 2, c4 = lane & 3;
+  kv_turns(a, turns, threadIdx.x, kThreads);  // kv_plan's barriers follow
+  for (int i = warp; i < D / 32; i += kWarps) {
+    const uint32_t b = __ballot_sync(0xffffffffu, a.k_signs != nullptr && __ldg(a.k_signs + 32 * i + lane) < 0);
+    if (lane == 0) k_neg[i] = b;
+  }
   const KvPlan plan = kv_plan<ROWS, TK, kThreads>(a, t, kWarps);
   const KvWork work = kv_work_of<D, ROWS>(t.ws, gridDim.x);
   KvPart open;
   open.first = -1;
+  const bool one_page = (1 << a.log_page) >= TK;
+  const uint32_t in_page = (1u << a.log_page) - 1;
+  uint8_t* const ring = smem + warp * F::STAGE;  // of this warp, a stage every kWarps * STAGE
+  auto page_at = [&](int s, int64_t p) {  // p >= 0 lies in the table: units end at KvSeq::hi
+    return __ldg(a.table + int64_t(s) * a.ld_table + (p >> a.log_page));
+  };
+  constexpr uint64_t kAll = TK == 64 ? ~uint64_t(0) : (uint64_t(1) << (TK & 63)) - 1;
 
   int s = plan.seq;
   int64_t base = plan.base;
@@ -142,40 +163,70 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
     const int64_t b1 = min(x1, (hi_max + TK - 1) / TK - q.unit0);
     const int nu = b0 + warp < b1 ? int((b1 - b0 - warp + kWarps - 1) / kWarps) : 0;
 
-    // Unit i of this warp into its stage i % kStages.
-    auto issue = [&](int i) {
-      if (i < nu) {
-        const uint32_t st = smem_u32(smem) + uint32_t(((i % kStages) * kWarps + warp) * F::STAGE);
-        const int64_t p0 = (q.unit0 + b0 + warp + int64_t(kWarps) * i) * TK;
-        int64_t at[(TK + 31) / 32];
+    // The warp's next unit into its next stage.  Where a unit lies inside a page
+    // (pages of at least TK positions) its vectors are one run of memory and the
+    // lane's pieces have fixed offsets; positions behind the sequence's end are
+    // then copied too (they are the page's) and hidden from every row later.  A
+    // missing page leaves the stage as it is: nothing of it is seen.
+    const int64_t head = int64_t(h) << a.log_page;
+    int next = 0, next_stage = 0;
+    int64_t next_p = (q.unit0 + b0 + warp) * TK;
+    int next_page = one_page && nu > 0 ? page_at(s, next_p) : -1;
+    auto issue = [&]() {
+      if (next < nu) {
+        uint8_t* const stp = ring + next_stage * (kWarps * F::STAGE);
+        const uint32_t st = smem_u32(stp);
         uint64_t there = 0;
+        if (one_page) {
+          const int page = next_page;
+          if (next + 1 < nu) next_page = page_at(s, next_p + kWarps * TK);
+          if (page >= 0 && page < a.pages) {
+            there = kAll;
+            const int64_t vec = ((int64_t(page) * a.hk) << a.log_page) + head + (uint32_t(next_p) & in_page);
+            const uint8_t* const kc = a.k_codes + vec * VB + 16 * lane;
+            const uint8_t* const vc = a.v_codes + vec * VB + 16 * lane;
 #pragma unroll
-        for (int k = 0; k < (TK + 31) / 32; ++k) {
-          const int64_t p = p0 + lane + 32 * k;
-          at[k] = lane + 32 * k < TK && p < q.hi ? kv_slot(a, s, p) : -1;
-          there |= uint64_t(__ballot_sync(0xffffffffu, at[k] >= 0)) << (32 * k);
-          const bool in = at[k] >= 0;
-          at[k] = in ? at[k] + (int64_t(h) << a.log_page) : 0;
-          if (lane + 32 * k < TK) {
-            copy4(st + 2 * TK * VB + 4 * (lane + 32 * k), a.k_scales + at[k], in);
-            copy4(st + 2 * TK * VB + 4 * (TK + lane + 32 * k), a.v_scales + at[k], in);
+            for (int k = 0; k < TK * CH / 32; ++k) {
+              const int tk = (32 * k) / CH + lane / CH;
+              copy16(st + 16 * k_place<CH>(tk, lane % CH), kc + 512 * k);
+              copy16(st + TK * VB + 16 * v_place<CH>(tk, lane % CH), vc + 512 * k);
+            }
+            if (lane < TK / 4) {
+              copy16(st + 2 * TK * VB + 16 * lane, a.k_scales + vec + 4 * lane);
+              copy16(st + 2 * TK * VB + 4 * TK + 16 * lane, a.v_scales + vec + 4 * lane);
+            }
+          }
+        } else {
+          int64_t at[(TK + 31) / 32];
+#pragma unroll
+          for (int k = 0; k < (TK + 31) / 32; ++k) {
+            const int64_t p = next_p + lane + 32 * k;
+            at[k] = lane + 32 * k < TK && p < q.hi ? kv_slot(a, s, p) : -1;
+            there |= uint64_t(__ballot_sync(0xffffffffu, at[k] >= 0)) << (32 * k);
+            if (at[k] >= 0) {
+              at[k] += head;
+              copy4(st + 2 * TK * VB + 4 * (lane + 32 * k), a.k_scales + at[k]);
+              copy4(st + 2 * TK * VB + 4 * (TK + lane + 32 * k), a.v_scales + at[k]);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < TK * CH / 32; ++k) {
+            const int tk = (32 * k) / CH + lane / CH, piece = lane % CH;
+            const int64_t vec = __shfl_sync(0xffffffffu, at[(32 * k) / CH / 32], tk & 31);
+            if (vec >= 0) {
+              copy16(st + 16 * k_place<CH>(tk, piece), a.k_codes + vec * VB + 16 * piece);
+              copy16(st + TK * VB + 16 * v_place<CH>(tk, piece), a.v_codes + vec * VB + 16 * piece);
+            }
           }
         }
-#pragma unroll
-        for (int k = 0; k < TK * CH / 32; ++k) {
-          const int tk = (32 * k) / CH + lane / CH, piece = lane % CH;
-          const int64_t vec = __shfl_sync(0xffffffffu, at[(32 * k) / CH / 32], tk & 31);
-          const bool in = (there >> tk) & 1;
-          copy16(st + 16 * k_place<CH>(tk, piece), a.k_codes + vec * VB + 16 * piece, in);
-          copy16(st + TK * VB + 16 * v_place<CH>(tk, piece), a.v_codes + vec * VB + 16 * piece, in);
-        }
-        if (lane == 0) {
-          *reinterpret_cast<uint64_t*>(smem + ((i % kStages) * kWarps + warp) * F::STAGE + TK * (2 * VB + 8)) = there;
-        }
+        if (lane == 0) *reinterpret_cast<uint64_t*>(stp + TK * (2 * VB + 8)) = there;
+        ++next;
+        next_p += kWarps * TK;
+        next_stage = next_stage == kStages - 1 ? 0 : next_stage + 1;
       }
       copies_commit();
     };
-    issue(0);
+    issue();
 
     // The tile's queries: turned, rotated, scaled (into base-2 scores), and
     // brought to [-2, 2) by a power of two; scratch in the stages behind the first.
@@ -185,9 +236,10 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
     {
       uint8_t* scratch = smem + kWarps * F::STAGE;
       float2* cs = reinterpret_cast<float2*>(scratch);
-      __half* qs = reinterpret_cast<__half*>(scratch + sizeof(float2) * ROWS * (D / 2));
-      float* es = reinterpret_cast<float*>(qs + ROWS * QP);
-      static_assert(sizeof(float2) * ROWS * (D / 2) + 2 * ROWS * QP + 4 * ROWS <= 2 * kWarps * F::STAGE, "scratch");
+      // [rows / 8][D / 32][8 rows][4 lanes] x 16 bytes: a lane's operands of eight elements
+      uint4* qs = reinterpret_cast<uint4*>(scratch + sizeof(float2) * ROWS * (D / 2));
+      float* es = reinterpret_cast<float*>(qs + ROWS * (D / 8));
+      static_assert(sizeof(float2) * ROWS * (D / 2) + 2 * ROWS * D + 4 * ROWS <= 2 * kWarps * F::STAGE, "scratch");
       for (int i = threadIdx.x; i < (i1 - i0 + 1) * a.n_freq; i += kThreads) {
         const int j = i / a.n_freq;
         cs[i] = kv_angle_fast(a, turns, q.t0 + i0 + j, int(q.pos0) + i0 + j, i - j * a.n_freq);
@@ -212,7 +264,14 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
             for (int c = 0; c < 4; ++c) kv_load8<false>(t.q, src + 8 * (c * LPV + l), x + 8 * c);
             if (a.n_freq > 0) kv_rope<D, false>(x, t.q, src, cs + (tok - i0) * a.n_freq, a.n_freq, a.interleaved, l);
           }
-          kv_signs<D>(x, a.k_signs, l);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int ch = c * LPV + l;
+            const uint32_t neg = k_neg[ch >> 2] >> (8 * (ch & 3));
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              x[8 * c + e] = __uint_as_float(__float_as_uint(x[8 * c + e]) ^ ((neg << (31 - e)) & 0x80000000u));
+          }
         }
         kv_hadamard<D>(x, l);
         float up, down;
@@ -223,10 +282,15 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
             uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const __half2 p = __floats2half2_rn(x[8 * c + 2 * e] * down, x[8 * c + 2 * e + 1] * down);
+              const int i = BITS == 4 ? e : 2 * e, j = BITS == 4 ? e + 4 : 2 * e + 1;
+              const __half2 p = __floats2half2_rn(x[8 * c + i] * down, x[8 * c + j] * down);
               w[e] = *reinterpret_cast<const uint32_t*>(&p);
             }
-            *reinterpret_cast<uint4*>(qs + r * QP + 8 * (c * LPV + l)) = make_uint4(w[0], w[1], w[2], w[3]);
+            // chunk of eight elements -> the lane (of four) that holds their codes, and its how manieth
+            const int ch = c * LPV + l;
+            const int owner = CH == 2 ? ch >> 1 : BITS == 4 ? (ch >> 2) & 3 : (ch >> 1) & 3;
+            const int at = CH == 2 ? ch & 1 : BITS == 4 ? 4 * (ch >> 4) + (ch & 3) : 2 * (ch >> 3) + (ch & 1);
+            qs[(((r >> 3) * (D / 32) + at) * 8 + (r & 7)) * 4 + owner] = make_uint4(w[0], w[1], w[2], w[3]);
           }
           if (l == 0) es[r] = up;
         }
@@ -234,21 +298,13 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
       __syncthreads();
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const uint16_t* row = reinterpret_cast<const uint16_t*>(qs + (8 * n + r8) * QP);
-        auto two = [&](int i, int j) { return uint32_t(row[i]) | (uint32_t(row[j]) << 16); };
 #pragma unroll
-        for (int w = 0; w < VB / 16; ++w) {  // the lane's words of a vector's codes
-          const int byte = CH == 2 ? 8 * c4 + 4 * w : 16 * (4 * (w / 4) + c4) + 4 * (w % 4);
-          if constexpr (BITS == 4) {
-            const int d = 2 * byte;
-            qf[2 * w][n][0] = two(d, d + 4);
-            qf[2 * w][n][1] = two(d + 1, d + 5);
-            qf[2 * w + 1][n][0] = two(d + 2, d + 6);
-            qf[2 * w + 1][n][1] = two(d + 3, d + 7);
-          } else {
-            qf[w][n][0] = two(byte, byte + 1);
-            qf[w][n][1] = two(byte + 2, byte + 3);
-          }
+        for (int w = 0; w < D / 32; ++w) {
+          const uint4 v = qs[((n * (D / 32) + w) * 8 + r8) * 4 + c4];
+          qf[2 * w][n][0] = v.x;
+          qf[2 * w][n][1] = v.y;
+          qf[2 * w + 1][n][0] = v.z;
+          qf[2 * w + 1][n][1] = v.w;
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -267,29 +323,32 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int i = 0; i < OM; ++i) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.0f;
-      m[n][0] = m[n][1] = -INFINITY;
+      // columns behind the tile's rows need no reference
+      m[n][0] = 8 * n + 2 * c4 < nr ? -INFINITY : 0.0f;
+      m[n][1] = 8 * n + 2 * c4 + 1 < nr ? -INFINITY : 0.0f;
       l[n][0] = l[n][1] = 0.0f;
     }
-    issue(1);
+    issue();
+    int stage = 0;
     for (int i = 0; i < nu; ++i) {
-      issue(i + 2);
+      issue();
       copies_wait<2>();
       __syncwarp();
-      uint8_t* stp = smem + ((i % kStages) * kWarps + warp) * F::STAGE;
+      uint8_t* const stp = ring + stage * (kWarps * F::STAGE);
+      stage = stage == kStages - 1 ? 0 : stage + 1;
       const uint32_t st = smem_u32(stp);
       const uint64_t there = *reinterpret_cast<const uint64_t*>(stp + TK * (2 * VB + 8));
       const float* ks = reinterpret_cast<const float*>(stp + 2 * TK * VB);
       const float* vs = ks + TK;
       const int64_t p0 = (q.unit0 + b0 + warp + int64_t(kWarps) * i) * TK;
-      const bool full = p0 >= lo_max && p0 + TK <= hi_min && there == (TK == 64 ? ~uint64_t(0) : (uint64_t(1) << (TK & 63)) - 1);
-      const int own = (r8 >> 1) + 4 * (r8 & 1);  // position of score row r8 within its 16
+      const bool full = p0 >= lo_max && p0 + TK <= hi_min && there == kAll;
 
       float sc[MT][NT][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) sc[mt][n][0] = sc[mt][n][1] = sc[mt][n][2] = sc[mt][n][3] = 0.0f;
-        const int tk = 16 * mt + own;
+        const int tk = 16 * mt + r8;
 #pragma unroll
         for (int j = 0; j < (CH == 2 ? 1 : CH / 4); ++j) {
           uint32_t wa[4], wb[4];
@@ -328,101 +387,123 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            sc[mt][n][e] *= (e < 2 ? k0 : k1) * qe[n][e & 1];
-            if (!full) {
-              const int w = tk + (e < 2 ? 0 : 8);
-              const int64_t p = p0 + w;
-              if (!((there >> w) & 1) || p < lo[n][e & 1] || p >= hi[n][e & 1]) sc[mt][n][e] = -INFINITY;
-            }
+            sc[mt][n][e] *= e < 2 ? k0 : k1;
           }
         }
+      }
+      if (!full) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int w = 16 * mt + r8 + (e < 2 ? 0 : 8);
+            const int p = int(p0) + w;
+            const bool in = (there >> w) & 1;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              if (!in || p < lo[n][e & 1] || p >= hi[n][e & 1]) sc[mt][n][e] = -INFINITY;
+          }
       }
 
-      // running maximum and sum of each column
-      bool moved = false;
-      float f[NT][2];
+      // Probabilities against the columns' references so far.  A reference is a
+      // maximum of scores seen before and is only raised where a lane's share of a
+      // column adds up to more than kGrow (bf16 and fp32 hold 2^16 as well as 1).
+      float pr[MT][NT][4], add[NT][2];
+      auto powers = [&]() {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+        for (int n = 0; n < NT; ++n) {
+          const float b0_ = m[n][0] == -INFINITY ? 0.0f : -m[n][0], b1_ = m[n][1] == -INFINITY ? 0.0f : -m[n][1];
+          add[n][0] = add[n][1] = 0.0f;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float v = m[n][k];
+          for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) v = fmaxf(v, fmaxf(sc[mt][n][k], sc[mt][n][k + 2]));
-#pragma unroll
-          for (int b = 4; b < 32; b <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, b));
-          moved |= v > m[n][k];
-          const float top = v == -INFINITY ? 0.0f : v;
-          f[n][k] = exp2f(m[n][k] - top);
-          m[n][k] = v;
-          float sum = 0.0f;
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-            for (int e = k; e < 4; e += 2) {
-              const bool hidden = !full && sc[mt][n][e] == -INFINITY;
-              const float p = exp2f(sc[mt][n][e] - top);
-              sum += p;
-              const float v_scale = vs[16 * mt + own + (e < 2 ? 0 : 8)];
-              sc[mt][n][e] = hidden ? 0.0f : p * v_scale;
+            for (int e = 0; e < 4; ++e) {
+              pr[mt][n][e] = ex2(fmaf(sc[mt][n][e], qe[n][e & 1], e & 1 ? b1_ : b0_));
+              add[n][e & 1] += pr[mt][n][e];
             }
-          }
-          l[n][k] = l[n][k] * f[n][k] + sum;
         }
-      }
-      if (__any_sync(0xffffffffu, moved)) {
+      };
+      powers();
+      bool grow = false;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) grow |= m[n][k] == -INFINITY || add[n][k] > kGrow;
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float f[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float v = -INFINITY;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) v = fmaxf(v, fmaxf(sc[mt][n][k], sc[mt][n][k + 2]));
+            v *= qe[n][k];
+#pragma unroll
+            for (int b = 4; b < 32; b <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, b));
+            // a column's lanes agree on v, and so on its new reference
+            f[k] = v > m[n][k] ? ex2(m[n][k] - v) : 1.0f;
+            m[n][k] = fmaxf(m[n][k], v);
+            l[n][k] *= f[k];
+          }
 #pragma unroll
           for (int d = 0; d < OM; ++d)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[d][n][e] *= f[n][e & 1];
+            for (int e = 0; e < 4; ++e) o[d][n][e] *= f[e & 1];
+        }
+        powers();
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        l[n][0] += add[n][0];
+        l[n][1] += add[n][1];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const float v0 = vs[16 * mt + r8], v1 = vs[16 * mt + r8 + 8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) pr[mt][n][e] *= e < 2 ? v0 : v1;
+        }
+      }
+      if (!full) {  // the scale of a hidden position may be anything
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) pr[mt][n][e] = sc[mt][n][e] == -INFINITY ? 0.0f : pr[mt][n][e];
       }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         uint32_t pb[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          pb[n][0] = transpose8x8(f32_to_bf16x2(sc[mt][n][0], sc[mt][n][1]));
-          pb[n][1] = transpose8x8(f32_to_bf16x2(sc[mt][n][2], sc[mt][n][3]));
+          pb[n][0] = transpose8x8(f32_to_bf16x2(pr[mt][n][0], pr[mt][n][1]));
+          pb[n][1] = transpose8x8(f32_to_bf16x2(pr[mt][n][2], pr[mt][n][3]));
         }
-        // the lane's D / 8 elements of four positions
-        constexpr int NW = VB / 32;
-        uint32_t v[4][NW];
+        // 16-bit units of codes, of two neighbouring positions a register: matrix
+        // lane / 8 of a load is positions 8 (lane / 8 % 2) ... of piece x or x + 1
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int tk = 16 * mt + c4 + 4 * g;
-          const uint32_t vb = st + TK * VB;
-          if constexpr (NW == 1) v[g][0] = lds32(vb + 16 * v_place<CH>(tk, r8 >> 2) + 4 * (r8 & 3));
-          if constexpr (NW == 2) lds64(vb + 16 * v_place<CH>(tk, r8 >> 1) + 8 * (r8 & 1), v[g]);
-          if constexpr (NW == 4) lds128(vb + 16 * v_place<CH>(tk, r8), v[g]);
-          if constexpr (NW == 8) {
-            lds128(vb + 16 * v_place<CH>(tk, 2 * r8), v[g]);
-            lds128(vb + 16 * v_place<CH>(tk, 2 * r8 + 1), v[g] + 4);
-          }
-        }
+        for (int x = 0; x < CH; x += 2) {
+          const int tk = 16 * mt + (lane & 15), piece = x + (lane >> 4);
+          uint32_t v[4];
+          load_transposed(st + TK * VB + 16 * v_place<CH>(tk, piece), v);
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const uint32_t ab = __byte_perm(v[0][w], v[1][w], half ? 0x7632 : 0x5410);
-            const uint32_t cd = __byte_perm(v[2][w], v[3][w], half ? 0x7632 : 0x5410);
+          for (int y = 0; y < 2; ++y) {  // positions 0-7 and 8-15 of piece x + y
             if constexpr (BITS == 4) {
-              uint32_t x[4], y[4];
-              bf_of4(ab, x);
-              bf_of4(cd, y);
-              const int d = 4 * w + 2 * half;
+              uint32_t ab[4], cd[4];
+              bf_of4(v[2 * y], ab);
+              bf_of4(v[2 * y + 1], cd);
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
-                mma_b16(o[d][n], x[0], x[1], y[0], y[1], pb[n][0], pb[n][1]);
-                mma_b16(o[d + 1][n], x[2], x[3], y[2], y[3], pb[n][0], pb[n][1]);
+                mma_b16(o[2 * (x + y)][n], ab[0], ab[1], cd[0], cd[1], pb[n][0], pb[n][1]);
+                mma_b16(o[2 * (x + y) + 1][n], ab[2], ab[3], cd[2], cd[3], pb[n][0], pb[n][1]);
               }
             } else {
-              uint32_t x0, x1_, y0, y1;
-              bf_of8(ab, x0, x1_);
-              bf_of8(cd, y0, y1);
-              const int d = 2 * w + half;
+              uint32_t a0, a1, c0, c1;
+              bf_of8(v[2 * y], a0, a1);
+              bf_of8(v[2 * y + 1], c0, c1);
 #pragma unroll
-              for (int n = 0; n < NT; ++n) mma_b16(o[d][n], x0, x1_, y0, y1, pb[n][0], pb[n][1]);
+              for (int n = 0; n < NT; ++n) mma_b16(o[x + y][n], a0, a1, c0, c1, pb[n][0], pb[n][1]);
             }
           }
         }
@@ -444,11 +525,17 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
         for (int b = 4; b < 32; b <<= 1) l[n][k] += __shfl_xor_sync(0xffffffffu, l[n][k], b);
         const int r = 8 * n + 2 * c4 + k;
         if (r8 == 0) ms[warp * ROWS + r] = make_float2(m[n][k], l[n][k]);
-        float* dst = mo + (warp * ROWS + r) * D + r8 * (D / 8);
+        float* dst = mo + (warp * ROWS + r) * D;
+        if constexpr (BITS == 4) {  // tiles 2 x and 2 x + 1: elements 32 x + 4 r8 ...
 #pragma unroll
-        for (int i = 0; i < OM; i += 2)
-          *reinterpret_cast<float4*>(dst + 2 * i) =
-              make_float4(o[i][n][k], o[i][n][k + 2], o[i + 1][n][k], o[i + 1][n][k + 2]);
+          for (int x = 0; x < CH; ++x)
+            *reinterpret_cast<float4*>(dst + 32 * x + 4 * r8) =
+                make_float4(o[2 * x][n][k], o[2 * x][n][k + 2], o[2 * x + 1][n][k], o[2 * x + 1][n][k + 2]);
+        } else {  // tile x: elements 16 x + 2 r8, + 1
+#pragma unroll
+          for (int x = 0; x < CH; ++x)
+            *reinterpret_cast<float2*>(dst + 16 * x + 2 * r8) = make_float2(o[x][n][k], o[x][n][k + 2]);
+        }
       }
     }
     __syncthreads();
@@ -523,7 +610,7 @@ cudaError_t go(const KvArgs& a, const KvAttn& t, cudaStream_t st) {
   kernel<<<ctas, kThreads, bytes, st>>>(a, t);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_kv_join<D, 8 * NT, 8 * NT>(a, t, ctas, st);
+  return launch_kv_join<D, 8 * NT, 1>(a, t, ctas, st);
 }
 
 }  // namespace

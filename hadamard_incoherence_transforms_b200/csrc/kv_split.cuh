@@ -198,7 +198,7 @@ __device__ __forceinline__ float kv_max(float a, float b) {
 // Joins the parts of the pairs that several CTAs share: block c handles the
 // pair that CTA c began and did not end (slot 2 c + 1), rows PER y ... of it.  A
 // row's parts are dealt to the warps left over by the number of rows.
-constexpr int kJoinWarps = 16;
+constexpr int kJoinWarps = 4;
 template <int D, int ROWS, int PER>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_kv_join(const KvArgs a, const KvAttn t, int ctas) {
   constexpr int E = D / 32;
