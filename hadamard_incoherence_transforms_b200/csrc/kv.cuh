@@ -130,6 +130,14 @@ __device__ __forceinline__ void kv_signs(float (&x)[32], const int8_t* __restric
   }
 }
 
+// The power of two of a row whose largest absolute element has the bits m, and
+// its reciprocal; 1 for an infinity or a NaN, which are left to spread.
+__device__ __forceinline__ void kv_row_power(uint32_t m, float& up, float& down) {
+  const uint32_t ex = max(1u, m >> 23);
+  const bool odd = ex == 255;
+  up = odd ? 1.0f : __uint_as_float(ex << 23);
+  down = odd ? 1.0f : __uint_as_float(ex == 254 ? 0x00400000u : (254 - ex) << 23);
+}
 // Unnormalised rotated query x to base-2 scores, and the power of two `up` of
 // the row's largest element with `down` = 1 / up: x * down is in [-2, 2), where
 // fp16 keeps it to half a step of 2^-10 of its largest element or better.
@@ -144,10 +152,7 @@ __device__ __forceinline__ void kv_query_scale(float (&x)[32], float scale, floa
   }
 #pragma unroll
   for (int b = 0; b < KvLanes<D>::LOG; ++b) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1 << b));
-  const uint32_t ex = max(1u, m >> 23);
-  const bool odd = ex == 255;  // an infinity or a NaN: left to spread
-  up = odd ? 1.0f : __uint_as_float(ex << 23);
-  down = odd ? 1.0f : __uint_as_float(ex == 254 ? 0x00400000u : (254 - ex) << 23);
+  kv_row_power(m, up, down);
 }
 
 // Eight consecutive elements as fp32.

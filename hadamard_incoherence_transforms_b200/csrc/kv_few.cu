@@ -39,7 +39,7 @@ template <int D, int BITS>
 struct Few {
   static constexpr int VB = D * BITS / 8;  // bytes of a vector's codes
   static constexpr int CH = VB / 16;
-  static constexpr int TK = VB == 32 ? 64 : VB == 64 ? 32 : VB == 128 ? (D == 256 ? 32 : 16) : 16;
+  static constexpr int TK = VB <= 64 ? 32 : VB == 128 ? (D == 256 ? 32 : 16) : 16;
   static constexpr int MT = TK / 16;
   static constexpr int STAGE = TK * (2 * VB + 8) + 16;
   static constexpr int KS = D / 16;
@@ -122,6 +122,8 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
   constexpr int OM = D / 16;   // 16-element tiles of the output's head dimension
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint64_t turns[D / 2];
+  __shared__ uint4 qs[ROWS * (D / 8)];  // [rows / 8][D / 32][8 rows][4 lanes]: a lane's operands of eight elements
+  __shared__ float es[ROWS];
   __shared__ uint32_t k_neg[D / 32];  // a bit for each element whose sign is flipped
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r8 = lane >> 2, c4 = lane & 3;
   kv_turns(a, turns, threadIdx.x, kThreads);  // kv_plan's barriers follow
@@ -226,73 +228,98 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
       }
       copies_commit();
     };
-    issue();
-
     // The tile's queries: turned, rotated, scaled (into base-2 scores), and
-    // brought to [-2, 2) by a power of two; scratch in the stages behind the first.
+    // brought to [-2, 2) by a power of two.  D / 8 threads a row, eight elements
+    // each; the first units are on their way meanwhile.
     uint32_t qf[KS][NT][2];
     float qe[NT][2];
     int lo[NT][2], hi[NT][2];
     {
-      uint8_t* scratch = smem + kWarps * F::STAGE;
-      float2* cs = reinterpret_cast<float2*>(scratch);
-      // [rows / 8][D / 32][8 rows][4 lanes] x 16 bytes: a lane's operands of eight elements
-      uint4* qs = reinterpret_cast<uint4*>(scratch + sizeof(float2) * ROWS * (D / 2));
-      float* es = reinterpret_cast<float*>(qs + ROWS * (D / 8));
-      static_assert(sizeof(float2) * ROWS * (D / 2) + 2 * ROWS * D + 4 * ROWS <= 2 * kWarps * F::STAGE, "scratch");
-      for (int i = threadIdx.x; i < (i1 - i0 + 1) * a.n_freq; i += kThreads) {
-        const int j = i / a.n_freq;
-        cs[i] = kv_angle_fast(a, turns, q.t0 + i0 + j, int(q.pos0) + i0 + j, i - j * a.n_freq);
-      }
-      __syncthreads();
-      constexpr int LPV = KvLanes<D>::LPV;
-      const int l = threadIdx.x % LPV;
-      for (int r0 = 0; r0 < ROWS; r0 += kThreads / LPV) {
-        const int r = r0 + int(threadIdx.x) / LPV;
-        float x[32];
+      constexpr int TPR = D / 8, PER = kThreads / TPR;
+      const int ch = threadIdx.x % TPR, i0e = 8 * ch;
+      float x[(ROWS + PER - 1) / PER][8];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = 0.0f;
+      for (int p = 0; p * PER < ROWS; ++p) {
+        const int r = p * PER + int(threadIdx.x) / TPR;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[p][e] = 0.0f;
         if (r < nr) {
           const int row = row0 + r, tok = row / t.group;
-          const int64_t src = (q.t0 + tok) * t.q_ts + (int64_t(h) * t.group + row - tok * t.group) * t.q_hs;
-          if (t.q_f32) {
+          const int64_t src = (q.t0 + tok) * t.q_ts + (int64_t(h) * t.group + row - tok * t.group) * t.q_hs + i0e;
+          if (t.q_f32) kv_load8<true>(t.q, src, x[p]);
+          else kv_load8<false>(t.q, src, x[p]);
+        }
+      }
+      issue();
+      issue();
 #pragma unroll
-            for (int c = 0; c < 4; ++c) kv_load8<true>(t.q, src + 8 * (c * LPV + l), x + 8 * c);
-            if (a.n_freq > 0) kv_rope<D, true>(x, t.q, src, cs + (tok - i0) * a.n_freq, a.n_freq, a.interleaved, l);
+      for (int p = 0; p * PER < ROWS; ++p) {
+        const int r = p * PER + int(threadIdx.x) / TPR;
+        float(&y)[8] = x[p];
+        if (a.n_freq > 0) {
+          const int tok = r < nr ? (row0 + r) / t.group : 0;
+          const int pos = int(q.pos0) + tok;
+          const bool low = i0e < a.n_freq, turned = i0e < 2 * a.n_freq;
+          if (a.interleaved) {
+            if (turned) {
+#pragma unroll
+              for (int e = 0; e < 8; e += 2) {
+                const float2 cs = kv_angle_fast(a, turns, q.t0 + tok, pos, (i0e + e) / 2);
+                const float u = y[e], w = y[e + 1];
+                y[e] = u * cs.x - w * cs.y;
+                y[e + 1] = u * cs.y + w * cs.x;
+              }
+            }
           } else {
+            // the partner chunk is n_freq elements on or back (n_freq % 8 == 0), with another lane of the row
+            const int shift = turned ? (low ? a.n_freq / 8 : -(a.n_freq / 8)) : 0;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) kv_load8<false>(t.q, src + 8 * (c * LPV + l), x + 8 * c);
-            if (a.n_freq > 0) kv_rope<D, false>(x, t.q, src, cs + (tok - i0) * a.n_freq, a.n_freq, a.interleaved, l);
-          }
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int ch = c * LPV + l;
-            const uint32_t neg = k_neg[ch >> 2] >> (8 * (ch & 3));
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              x[8 * c + e] = __uint_as_float(__float_as_uint(x[8 * c + e]) ^ ((neg << (31 - e)) & 0x80000000u));
+            for (int e = 0; e < 8; ++e) {
+              const float w = __shfl_sync(0xffffffffu, y[e], lane + shift);
+              if (turned) {
+                const float2 cs = kv_angle_fast(a, turns, q.t0 + tok, pos, (low ? i0e : i0e - a.n_freq) + e);
+                y[e] = low ? y[e] * cs.x - w * cs.y : w * cs.y + y[e] * cs.x;
+              }
+            }
           }
         }
-        kv_hadamard<D>(x, l);
-        float up, down;
-        kv_query_scale<D>(x, t.scale, up, down);
-        if (r < ROWS) {
+        const uint32_t neg = k_neg[ch >> 2] >> (8 * (ch & 3));
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t w[4];
+        for (int e = 0; e < 8; ++e)
+          y[e] = __uint_as_float(__float_as_uint(y[e]) ^ ((neg << (31 - e)) & 0x80000000u));
+        reg_stages<8, 0, 3>(y);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int i = BITS == 4 ? e : 2 * e, j = BITS == 4 ? e + 4 : 2 * e + 1;
-              const __half2 p = __floats2half2_rn(x[8 * c + i] * down, x[8 * c + j] * down);
-              w[e] = *reinterpret_cast<const uint32_t*>(&p);
-            }
-            // chunk of eight elements -> the lane (of four) that holds their codes, and its how manieth
-            const int ch = c * LPV + l;
-            const int owner = CH == 2 ? ch >> 1 : BITS == 4 ? (ch >> 2) & 3 : (ch >> 1) & 3;
-            const int at = CH == 2 ? ch & 1 : BITS == 4 ? 4 * (ch >> 4) + (ch & 3) : 2 * (ch >> 3) + (ch & 1);
-            qs[(((r >> 3) * (D / 32) + at) * 8 + (r & 7)) * 4 + owner] = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int b = 1; b < TPR; b <<= 1) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float w = __shfl_xor_sync(0xffffffffu, y[e], b);
+            y[e] = ch & b ? w - y[e] : y[e] + w;
           }
-          if (l == 0) es[r] = up;
+        }
+        const float f = (D == 64 ? 0.125f : D == 256 ? 0.0625f : 0.08838834764831845f) * 1.4426950408889634f * t.scale;
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          y[e] *= f;
+          top = max(top, __float_as_uint(y[e]) & 0x7fffffffu);
+        }
+#pragma unroll
+        for (int b = 1; b < TPR; b <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, b));
+        float up, down;
+        kv_row_power(top, up, down);
+        if (r < ROWS) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = BITS == 4 ? e : 2 * e, j = BITS == 4 ? e + 4 : 2 * e + 1;
+            const __half2 v = __floats2half2_rn(y[i] * down, y[j] * down);
+            w[e] = *reinterpret_cast<const uint32_t*>(&v);
+          }
+          // the chunk goes to the lane (of four) that holds its codes, as its how manieth
+          const int owner = CH == 2 ? ch >> 1 : BITS == 4 ? (ch >> 2) & 3 : (ch >> 1) & 3;
+          const int at = CH == 2 ? ch & 1 : BITS == 4 ? 4 * (ch >> 4) + (ch & 3) : 2 * (ch >> 3) + (ch & 1);
+          qs[(((r >> 3) * (D / 32) + at) * 8 + (r & 7)) * 4 + owner] = make_uint4(w[0], w[1], w[2], w[3]);
+          if (ch == 0) es[r] = up;
         }
       }
       __syncthreads();
@@ -315,7 +342,6 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
           lo[n][k] = t.window > 0 ? int(max(int64_t(0), min(q.hi, pos - t.window + 1))) : 0;
         }
       }
-      __syncthreads();
     }
 
     float o[OM][NT][4], m[NT][2], l[NT][2];
@@ -328,7 +354,6 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
       m[n][1] = 8 * n + 2 * c4 + 1 < nr ? -INFINITY : 0.0f;
       l[n][0] = l[n][1] = 0.0f;
     }
-    issue();
     int stage = 0;
     for (int i = 0; i < nu; ++i) {
       issue();
