@@ -32,6 +32,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStages = 3;
 constexpr float kGrow = 65536.0f;
+constexpr int kLead = 16;  // beginning a pair takes a CTA about as long as 16 units
 
 // Positions of a unit: stages of about 4 KB (8 KB for heads of 256), which is
 // 16 warps x 2 stages = 140 KB in flight on an SM.
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
     const uint32_t b = __ballot_sync(0xffffffffu, a.k_signs != nullptr && __ldg(a.k_signs + 32 * i + lane) < 0);
     if (lane == 0) k_neg[i] = b;
   }
-  const KvPlan plan = kv_plan<ROWS, TK, kThreads>(a, t, kWarps);
+  const KvPlan plan = kv_plan<ROWS, TK, kLead, kThreads>(a, t, kWarps);
   const KvWork work = kv_work_of<D, ROWS>(t.ws, gridDim.x);
   KvPart open;
   open.first = -1;
@@ -146,12 +147,17 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
   int s = plan.seq;
   int64_t base = plan.base;
   KvSeq q{};
-  if (s < a.seqs) q = kv_seq<ROWS, TK>(a, t, s);
+  if (s < a.seqs) q = kv_seq<ROWS, TK, kLead>(a, t, s);
   for (int64_t u = plan.u0; u < plan.u1;) {
     const int64_t rel = u - base;
     const int64_t pair = rel / q.units;
     const int64_t x0 = rel - pair * q.units;
     const int64_t x1 = min(q.units, x0 + plan.u1 - u);
+    const bool begins = x0 <= kLead;  // no unit of the pair's keys lies in an earlier CTA's share
+    if (x1 <= kLead) {                // and none in this one's
+      u += x1 - x0;
+      continue;
+    }
     const int h = int(pair / q.row_tiles), rt = int(pair - int64_t(h) * q.row_tiles);
     const int row0 = rt * ROWS;
     const int nr = int(min(int64_t(ROWS), int64_t(q.n) * t.group - row0));
@@ -161,8 +167,8 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
     const int64_t hi_max = t.causal ? min(q.hi, q.pos0 + i1 + 1) : q.hi;
     const int64_t lo_min = t.window > 0 ? max(int64_t(0), q.pos0 + i0 - t.window + 1) : 0;
     const int64_t lo_max = t.window > 0 ? max(int64_t(0), q.pos0 + i1 - t.window + 1) : 0;
-    const int64_t b0 = max(x0, lo_min / TK - q.unit0);
-    const int64_t b1 = min(x1, (hi_max + TK - 1) / TK - q.unit0);
+    const int64_t b0 = max(max(x0 - kLead, int64_t(0)), lo_min / TK - q.unit0);
+    const int64_t b1 = min(x1 - kLead, (hi_max + TK - 1) / TK - q.unit0);
     const int nu = b0 + warp < b1 ? int((b1 - b0 - warp + kWarps - 1) / kWarps) : 0;
 
     // The warp's next unit into its next stage.  Where a unit lies inside a page
@@ -564,8 +570,8 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
       }
     }
     __syncthreads();
-    const bool whole = x0 == 0 && x1 == q.units;
-    const size_t slot = x0 == 0 ? 2 * blockIdx.x + 1 : 2 * blockIdx.x;
+    const bool whole = begins && x1 == q.units;
+    const size_t slot = begins ? 2 * blockIdx.x + 1 : 2 * blockIdx.x;
     constexpr int E = D / 32;
     for (int r = warp; r < nr; r += kWarps) {
       float top = ms[r].x;
@@ -595,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
         if (lane == 0) work.ms[slot * ROWS + r] = make_float2(top, sum);
       }
     }
-    if (!whole && x0 == 0) {
+    if (!whole && begins) {
       open.first = blockIdx.x;
       open.last = kv_cta_of(base + (pair + 1) * q.units - 1, plan.total, plan.ctas);
       open.rows = nr;
@@ -609,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
     if (u < plan.u1 && u >= base + kv_work(a, t, q)) {
       base += kv_work(a, t, q);
       do {
-        q = kv_seq<ROWS, TK>(a, t, ++s);
+        q = kv_seq<ROWS, TK, kLead>(a, t, ++s);
       } while (kv_work(a, t, q) == 0);
     }
   }

@@ -93,7 +93,7 @@ __device__ __forceinline__ int64_t chunk_units(const KvArgs& a, const KvAttn& t,
   int64_t w = 0;
   bool big = false;
   if (s0 + lane < a.seqs) {
-    const KvSeq q = kv_seq<kRows, kKeys>(a, t, s0 + lane);
+    const KvSeq q = kv_seq<kRows, kKeys, 0>(a, t, s0 + lane);
     if (kv_mine(t, q)) {
       big = q.row_tiles > 4;
       for (int rt = 0; rt < q.row_tiles && !big; ++rt) {
@@ -105,7 +105,7 @@ __device__ __forceinline__ int64_t chunk_units(const KvArgs& a, const KvAttn& t,
   }
   for (uint32_t m = __ballot_sync(0xffffffffu, big); m; m &= m - 1) {
     const int k = __ffs(m) - 1;
-    const int64_t v = head_units_warp(t, kv_seq<kRows, kKeys>(a, t, s0 + k), lane);
+    const int64_t v = head_units_warp(t, kv_seq<kRows, kKeys, 0>(a, t, s0 + k), lane);
     if (lane == k) w = v;
   }
   return w * a.hk;
@@ -143,7 +143,7 @@ __device__ __forceinline__ void plan_warp(const KvArgs& a, const KvAttn& t, Bars
   }
   int h = 0, rt = 0, x0 = 0;
   if (seq < a.seqs) {
-    const KvSeq q = kv_seq<kRows, kKeys>(a, t, seq);
+    const KvSeq q = kv_seq<kRows, kKeys, 0>(a, t, seq);
     const int64_t per = head_units_warp(t, q, lane);
     h = int((u0 - base) / per);
     int64_t r = u0 - base - h * per;
@@ -207,7 +207,7 @@ __device__ __forceinline__ bool walk(const KvArgs& a, const KvAttn& t, const Bar
   int s = b->seq, h = b->h, rt = b->rt, x0 = b->x0;
   int64_t left = b->units, at = int64_t(blockIdx.x) * b->total / b->ctas;
   KvSeq q{};
-  if (left > 0) q = kv_seq<kRows, kKeys>(a, t, s);
+  if (left > 0) q = kv_seq<kRows, kKeys, 0>(a, t, s);
   for (int n = 0;; ++n) {
     if (n >= kSegments && !mbar_wait(&ring->empty[n % kSegments], uint32_t(n / kSegments - 1) & 1u)) return false;
     if (*abort) return true;
@@ -258,7 +258,7 @@ __device__ __forceinline__ bool walk(const KvArgs& a, const KvAttn& t, const Bar
           if (++h == a.hk) {
             h = 0;
             do {
-              q = kv_seq<kRows, kKeys>(a, t, ++s);
+              q = kv_seq<kRows, kKeys, 0>(a, t, ++s);
             } while (q.n == 0 || !kv_mine(t, q));
           }
         }

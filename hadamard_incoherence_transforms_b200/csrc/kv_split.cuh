@@ -18,12 +18,15 @@ struct KvSeq {
   int64_t pos0;     // position of the first token
   int64_t hi;       // positions that can exist: [0, hi)
   int64_t unit0;    // first unit any row sees
-  int64_t units;    // units of a pair (at least one, so that every row is written)
+  int64_t units;    // units of a pair: `lead` empty ones, then those of its keys (at least
+                    // one, so that every row is written)
   int row_tiles;
 };
 
-// ROWS query rows to a tile, TK positions to a unit.
-template <int ROWS, int TK>
+// ROWS query rows to a tile, TK positions to a unit, LEAD empty units ahead of a
+// pair's: what beginning a pair costs, so that CTAs with many short pairs get
+// fewer positions.
+template <int ROWS, int TK, int LEAD>
 __device__ __forceinline__ KvSeq kv_seq(const KvArgs& a, const KvAttn& t, int s) {
   KvSeq q;
   const int64_t b = __ldg(a.cu + s), e = __ldg(a.cu + s + 1), len = __ldg(a.lens + s);
@@ -35,7 +38,7 @@ __device__ __forceinline__ KvSeq kv_seq(const KvArgs& a, const KvAttn& t, int s)
   int64_t lo = 0;
   if (t.window > 0) lo = min(q.hi, max(int64_t(0), q.pos0 - t.window + 1));
   q.unit0 = lo / TK;
-  q.units = max(int64_t(1), (q.hi + TK - 1) / TK - q.unit0);
+  q.units = LEAD + max(int64_t(1), (q.hi + TK - 1) / TK - q.unit0);
   const int64_t rows = int64_t(q.n) * t.group;
   q.row_tiles = int((rows + ROWS - 1) / ROWS);
   return q;
@@ -59,7 +62,7 @@ struct KvPlan {
 };
 
 // All `THREADS` threads of the CTA.  least: units that a CTA has at least.
-template <int ROWS, int TK, int THREADS>
+template <int ROWS, int TK, int LEAD, int THREADS>
 __device__ __forceinline__ KvPlan kv_plan(const KvArgs& a, const KvAttn& t, int least) {
   __shared__ int64_t sums[THREADS / 32];
   __shared__ int64_t found_base;
@@ -67,7 +70,7 @@ __device__ __forceinline__ KvPlan kv_plan(const KvArgs& a, const KvAttn& t, int 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   KvPlan p;
   int64_t mine = 0;
-  for (int s = threadIdx.x; s < a.seqs; s += THREADS) mine += kv_work(a, t, kv_seq<ROWS, TK>(a, t, s));
+  for (int s = threadIdx.x; s < a.seqs; s += THREADS) mine += kv_work(a, t, kv_seq<ROWS, TK, LEAD>(a, t, s));
   int64_t w = mine;
 #pragma unroll
   for (int b = 16; b; b >>= 1) w += __shfl_xor_sync(0xffffffffu, w, b);
@@ -85,7 +88,7 @@ __device__ __forceinline__ KvPlan kv_plan(const KvArgs& a, const KvAttn& t, int 
   int64_t before = 0;
   for (int s0 = 0; s0 < a.seqs; s0 += THREADS) {
     const int s = s0 + int(threadIdx.x);
-    const int64_t v = a.seqs <= THREADS ? mine : s < a.seqs ? kv_work(a, t, kv_seq<ROWS, TK>(a, t, s)) : 0;
+    const int64_t v = a.seqs <= THREADS ? mine : s < a.seqs ? kv_work(a, t, kv_seq<ROWS, TK, LEAD>(a, t, s)) : 0;
     int64_t x = v;
 #pragma unroll
     for (int b = 1; b < 32; b <<= 1) {
@@ -222,31 +225,42 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_kv_join(const KvArgs a, con
 #pragma unroll
     for (int e = 0; e < E; ++e) x[e] = 0.0f;
     if (in < rows) {
-      for (int i = team + lane * teams; i < parts; i += 32 * teams)
-        m = kv_max(m, w.ms[size_t(i == 0 ? 2 * c + 1 : 2 * (c + i)) * ROWS + r].x);
+      // this team's parts are team + j teams; their (max, sum) first, a lane a part,
+      // then the rows, whose loads wait for nothing
+      const int count = (parts - team + teams - 1) / teams;
+      auto place = [&](int j) {
+        const int i = team + j * teams;
+        return size_t(i == 0 ? 2 * c + 1 : 2 * (c + i)) * ROWS + r;
+      };
+      for (int j = lane; j < count; j += 32) m = kv_max(m, w.ms[place(j)].x);
 #pragma unroll
       for (int b = 16; b; b >>= 1) m = kv_max(m, __shfl_xor_sync(0xffffffffu, m, b));
-#pragma unroll 4
-      for (int i = team; i < parts; i += teams) {
-        const size_t row = size_t(i == 0 ? 2 * c + 1 : 2 * (c + i)) * ROWS + r;
-        const float2 q = __ldcs(w.ms + row);
-        const float f = kv_weight(q.x, m);
-        l = fmaf(f, q.y, l);
-        const float* src = w.rows + row * D + E * lane;
-        float v[E];
-        if constexpr (E == 2) {
-          const float2 u = __ldcs(reinterpret_cast<const float2*>(src));
-          v[0] = u.x, v[1] = u.y;
-        } else {
+      for (int j0 = 0; j0 < count; j0 += 32) {
+        const float2 q = j0 + lane < count ? w.ms[place(j0 + lane)] : make_float2(-INFINITY, 0.0f);
+        const float mine = kv_weight(q.x, m);
+        l = fmaf(mine, q.y, l);
+        const int n = min(32, count - j0);
+#pragma unroll 8
+        for (int j = 0; j < n; ++j) {
+          const float f = __shfl_sync(0xffffffffu, mine, j);
+          const float* src = w.rows + place(j0 + j) * D + E * lane;
+          float v[E];
+          if constexpr (E == 2) {
+            const float2 u = __ldcs(reinterpret_cast<const float2*>(src));
+            v[0] = u.x, v[1] = u.y;
+          } else {
 #pragma unroll
-          for (int e = 0; e < E; e += 4) {
-            const float4 u = __ldcs(reinterpret_cast<const float4*>(src + e));
-            v[e] = u.x, v[e + 1] = u.y, v[e + 2] = u.z, v[e + 3] = u.w;
+            for (int e = 0; e < E; e += 4) {
+              const float4 u = __ldcs(reinterpret_cast<const float4*>(src + e));
+              v[e] = u.x, v[e + 1] = u.y, v[e + 2] = u.z, v[e + 3] = u.w;
+            }
           }
-        }
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = fmaf(f, v[e], x[e]);
+          for (int e = 0; e < E; ++e) x[e] = fmaf(f, v[e], x[e]);
+        }
       }
+#pragma unroll
+      for (int b = 16; b; b >>= 1) l += __shfl_xor_sync(0xffffffffu, l, b);
     }
     if (teams > 1) {
 #pragma unroll
