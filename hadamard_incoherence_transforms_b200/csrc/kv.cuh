@@ -46,13 +46,26 @@ __device__ __forceinline__ int64_t kv_slot(const KvArgs& a, int s, int64_t p) {
 // Token t of the call (whole warp, same t).
 __device__ __forceinline__ KvToken kv_token(const KvArgs& a, int64_t t, int lane) {
   KvToken k{-1, 0, -1};
-  const int c = kv_count_le(a.cu, a.seqs, t, lane);
-  if (c < 1 || c > a.seqs) return k;
-  const int s = c - 1;
-  const int64_t b = __ldg(a.cu + s), e = __ldg(a.cu + s + 1);
+  int64_t b, e, len;
+  int s;
+  if (a.seqs < 32) {  // every boundary and length is some lane's: one round of loads
+    const int cu = lane <= a.seqs ? __ldg(a.cu + lane) : 0;
+    const int ln = lane < a.seqs ? __ldg(a.lens + lane) : 0;
+    const int c = __popc(__ballot_sync(0xffffffffu, lane <= a.seqs && cu <= t));
+    if (c < 1 || c > a.seqs) return k;
+    s = c - 1;
+    b = __shfl_sync(0xffffffffu, cu, s);
+    e = __shfl_sync(0xffffffffu, cu, c);
+    len = __shfl_sync(0xffffffffu, ln, s);
+  } else {
+    const int c = kv_count_le(a.cu, a.seqs, t, lane);
+    if (c < 1 || c > a.seqs) return k;
+    s = c - 1;
+    b = __ldg(a.cu + s), e = __ldg(a.cu + s + 1), len = __ldg(a.lens + s);
+  }
   if (t < b || t >= e) return k;
   k.seq = s;
-  k.pos = int64_t(__ldg(a.lens + s)) - (e - b) + (t - b);
+  k.pos = len - (e - b) + (t - b);
   k.slot = kv_slot(a, s, k.pos);
   return k;
 }
@@ -130,6 +143,27 @@ __device__ __forceinline__ void kv_signs(float (&x)[32], const int8_t* __restric
   }
 }
 
+// Table of signs times `norm` for the elements of a head, by the whole CTA.
+template <int D>
+__device__ __forceinline__ void kv_factors(float* f, const int8_t* __restrict__ signs, float norm) {
+  for (int i = threadIdx.x; i < D; i += blockDim.x) f[i] = signs != nullptr && __ldg(signs + i) < 0 ? -norm : norm;
+}
+// x <- x * f elementwise, f a table of the head's elements.
+template <int D>
+__device__ __forceinline__ void kv_times(float (&x)[32], const float* f, int l) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const float4* q = reinterpret_cast<const float4*>(f + 8 * (c * KvLanes<D>::LPV + l));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float4 g = q[h];
+      float* y = x + 8 * c + 4 * h;
+      mul_x2(y[0], y[1], g.x, g.y);
+      mul_x2(y[2], y[3], g.z, g.w);
+    }
+  }
+}
+
 // The power of two of a row whose largest absolute element has the bits m, and
 // its reciprocal; 1 for an infinity or a NaN, which are left to spread.
 __device__ __forceinline__ void kv_row_power(uint32_t m, float& up, float& down) {
@@ -200,6 +234,17 @@ __device__ __forceinline__ void kv_rope(float (&x)[32], const void* p, int64_t a
         const float u = v[e], w = v[e + 1];
         v[e] = u * t.x - w * t.y;
         v[e + 1] = u * t.y + w * t.x;
+      }
+    } else if (2 * n_freq == D) {  // both chunks of a pair are the lane's own
+      if (c >= 2) continue;
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        const float4 t = *reinterpret_cast<const float4*>(cs + i0 + e);
+        const float u0 = v[e], u1 = v[e + 1], w0 = v[16 + e], w1 = v[17 + e];
+        v[e] = u0 * t.x - w0 * t.y;
+        v[16 + e] = u0 * t.y + w0 * t.x;
+        v[e + 1] = u1 * t.z - w1 * t.w;
+        v[17 + e] = u1 * t.w + w1 * t.z;
       }
     } else {
       // the partner chunk lies n_freq elements on or back (n_freq % 8 == 0)

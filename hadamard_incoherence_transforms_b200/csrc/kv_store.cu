@@ -14,37 +14,43 @@ namespace hit {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTile = 16;  // tokens per CTA
+constexpr int kMaxTile = 8;  // tokens per CTA
 
-// Eight stored codes of t = y / s, by the correctly rounded quotient: q0 = y r
-// with r = RN(1/s), one correction step (exact remainder), and the code in the
-// low byte of t + 1.5 * 2^23 + 2^(b-1) (ties to even).
-__device__ __forceinline__ uint32_t kv_code(float y, float s, float r, float magic) {
-  const float q0 = y * r;
-  const float e = fmaf(-s, q0, y);
-  return __float_as_uint(fmaf(e, r, q0) + magic);
+// max that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 
-// Codes of the vector x (already normalised) and its scale.  All LPV lanes of
-// the vector call it together; the absmax is taken over bit patterns, where a
-// NaN is above everything, so that it reaches the scale.
+// Stored codes of the vector x and its scale.  All LPV lanes of the vector call it
+// together.  The usual case takes t = y / s by the correctly rounded quotient:
+// q0 = y r with r = RN(1/s), one correction step (exact remainder), and the code in
+// the low byte of t + 1.5 * 2^23 + 2^(b-1) (ties to even), on pairs.
 template <int D, int BITS>
-__device__ __forceinline__ float kv_quantize(float (&x)[32], uint32_t (&w)[4 * BITS / 4]) {
+__device__ __forceinline__ float kv_quantize(float (&x)[32], uint32_t (&w)[BITS]) {
   constexpr int QMAX = (1 << (BITS - 1)) - 1;
   constexpr float MAGIC = 12582912.0f + float(1 << (BITS - 1));
-  uint32_t m = 0;
+  float a = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
+  for (int i = 0; i < 32; ++i) a = max_nan(a, fabsf(x[i]));
 #pragma unroll
-  for (int b = 0; b < KvLanes<D>::LOG; ++b) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1 << b));
-  const float a = __uint_as_float(m);
+  for (int b = 0; b < KvLanes<D>::LOG; ++b) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, 1 << b));
   float s = __fdiv_rn(a, float(QMAX));
-  if (m >= 0x7f800000u) s = __uint_as_float(0x7fc00000u);
+  if (!(a < INFINITY)) s = __uint_as_float(0x7fc00000u);
   uint32_t u[32];
   if (a > 7.9e-31f && a < 1.2e30f) {  // quotient, remainder and reciprocal stay normal
     const float r = __frcp_rn(s);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) u[i] = kv_code(x[i], s, r, MAGIC);
+    for (int i = 0; i < 32; i += 2) {
+      float q0 = x[i], q1 = x[i + 1], e0, e1;
+      mul_x2(q0, q1, r, r);
+      fma_x2(q0, q1, -s, -s, x[i], x[i + 1], e0, e1);
+      fma_x2(e0, e1, r, r, q0, q1, q0, q1);
+      fma_x2(q0, q1, 1.0f, 1.0f, MAGIC, MAGIC, q0, q1);
+      u[i] = __float_as_uint(q0);
+      u[i + 1] = __float_as_uint(q1);
+    }
   } else {
     const bool live = s > 0.0f;  // false for s = 0 and for NaN
 #pragma unroll
@@ -65,61 +71,99 @@ __device__ __forceinline__ float kv_quantize(float (&x)[32], uint32_t (&w)[4 * B
   return s;
 }
 
+// Codes of eight elements (4 or 8 bytes) as fp32: the byte under 2^23's exponent,
+// minus 2^23 and the offset, exact.
+template <int BITS>
+__device__ __forceinline__ void kv_dequantize(const uint32_t* w, float* z) {
+  constexpr float OFF = -(8388608.0f + float(1 << (BITS - 1)));
+  const uint32_t a = BITS == 4 ? w[0] & 0x0f0f0f0fu : w[0], b = BITS == 4 ? (w[0] >> 4) & 0x0f0f0f0fu : w[1];
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    // 4 bits: a holds the even elements, b the odd ones; 8 bits: a the first four
+    const uint32_t w0 = BITS == 4 ? a : e < 4 ? a : b, w1 = BITS == 4 ? b : w0;
+    const int i0 = BITS == 4 ? e / 2 : e % 4, i1 = BITS == 4 ? e / 2 : e % 4 + 1;
+    float x0 = __uint_as_float(__byte_perm(w0, 0x4b000000u, 0x7650 | i0));
+    float x1 = __uint_as_float(__byte_perm(w1, 0x4b000000u, 0x7650 | i1));
+    fma_x2(x0, x1, 1.0f, 1.0f, OFF, OFF, z[e], z[e + 1]);
+  }
+}
+
 struct Tile {
   KvToken tok[kMaxTile];
 };
 
+// A CTA's tile of tokens; vector v of it is token v / (2 hk), keys of all heads
+// before values.
 template <int D, int BITS, bool F32>
 __global__ void __launch_bounds__(kThreads) k_kv_append(const KvArgs a, const KvDense x, int tile, float norm) {
   constexpr int LPV = KvLanes<D>::LPV;
-  extern __shared__ float2 cs[];  // [tile][n_freq]
+  extern __shared__ __align__(16) float2 cs[];  // [tile][n_freq]
   __shared__ Tile tl;
   __shared__ uint64_t turns[D / 2];
+  __shared__ __align__(16) float factors[2][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
   const int64_t t0 = int64_t(blockIdx.x) * tile;
   const int nt = int(min(int64_t(tile), a.tokens - t0));
+  const int l = threadIdx.x % LPV;
+  const int vectors = nt * 2 * a.hk, per = blockDim.x / LPV;
+  struct Place {
+    int j, h;
+    bool in, is_v;
+  };
+  auto place = [&](int v) {
+    Place p;
+    p.in = v < vectors;
+    p.j = p.in ? v / (2 * a.hk) : 0;
+    const int r = p.in ? v - p.j * 2 * a.hk : 0;
+    p.is_v = r >= a.hk;
+    p.h = p.is_v ? r - a.hk : r;
+    return p;
+  };
+  float y[32];
+  auto load = [&](const Place& p) {
+    const void* src = p.is_v ? x.v : x.k;
+    const int64_t at = (t0 + p.j) * (p.is_v ? x.v_ts : x.k_ts) + p.h * (p.is_v ? x.v_hs : x.k_hs);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (p.in) {
+        kv_load8<F32>(src, at + 8 * (c * LPV + l), y + 8 * c);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[8 * c + e] = 0.0f;
+      }
+    }
+  };
+  Place p = place(threadIdx.x / LPV);
+  load(p);  // the first vectors are on their way while their places are found
   for (int j = warp; j < nt; j += nw) {
     const KvToken k = kv_token(a, t0 + j, lane);
     if (lane == 0) tl.tok[j] = k;
   }
   kv_turns(a, turns, threadIdx.x, blockDim.x);
+  kv_factors<D>(factors[0], a.k_signs, norm);
+  kv_factors<D>(factors[1], a.v_signs, norm);
   __syncthreads();
   for (int i = threadIdx.x; i < nt * a.n_freq; i += blockDim.x) {
     const int j = i / a.n_freq, f = i - j * a.n_freq;
     if (tl.tok[j].slot >= 0) cs[i] = kv_angle(a, turns, t0 + j, int(tl.tok[j].pos), f);
   }
   __syncthreads();
-  const int l = threadIdx.x % LPV;
-  const int vectors = nt * 2 * a.hk;
-  const int per = blockDim.x / LPV;
   for (int v0 = 0; v0 < vectors; v0 += per) {  // every lane stays in the loop for the shuffles
-    const int v = v0 + int(threadIdx.x) / LPV;
-    const bool in = v < vectors;
-    const int j = in ? v / (2 * a.hk) : 0;
-    const int r = in ? v - j * 2 * a.hk : 0;
-    const bool is_v = r >= a.hk;
-    const int h = is_v ? r - a.hk : r;
-    const int64_t slot = tl.tok[j].slot;
-    const bool live = in && slot >= 0;
-    float y[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) y[i] = 0.0f;
-    if (live) {
-      const void* src = is_v ? x.v : x.k;
-      const int64_t at = (t0 + j) * (is_v ? x.v_ts : x.k_ts) + h * (is_v ? x.v_hs : x.k_hs);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) kv_load8<F32>(src, at + 8 * (c * LPV + l), y + 8 * c);
-      if (!is_v && a.n_freq > 0) kv_rope<D, F32>(y, src, at, cs + j * a.n_freq, a.n_freq, a.interleaved, l);
-      kv_signs<D>(y, is_v ? a.v_signs : a.k_signs, l);
+    if (v0 > 0) {
+      p = place(v0 + int(threadIdx.x) / LPV);
+      load(p);
     }
+    const int64_t slot = tl.tok[p.j].slot;
+    const bool live = p.in && slot >= 0;
+    if (live && !p.is_v && a.n_freq > 0)
+      kv_rope<D, F32>(y, x.k, (t0 + p.j) * x.k_ts + p.h * x.k_hs, cs + p.j * a.n_freq, a.n_freq, a.interleaved, l);
+    kv_times<D>(y, factors[p.is_v], l);
     kv_hadamard<D>(y, l);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) y[i] *= norm;
-    uint32_t w[4 * BITS / 4];
+    uint32_t w[BITS];
     const float s = kv_quantize<D, BITS>(y, w);
     if (live) {
-      const int64_t vec = slot + (int64_t(h) << a.log_page);
-      uint8_t* dst = (is_v ? a.v_codes : a.k_codes) + vec * (D * BITS / 8);
+      const int64_t vec = slot + (int64_t(p.h) << a.log_page);
+      uint8_t* dst = (p.is_v ? a.v_codes : a.k_codes) + vec * (D * BITS / 8);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         if constexpr (BITS == 4)
@@ -127,7 +171,7 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(const KvArgs a, const Kv
         else
           reinterpret_cast<uint2*>(dst)[c * LPV + l] = make_uint2(w[2 * c], w[2 * c + 1]);
       }
-      if (l == 0) (is_v ? a.v_scales : a.k_scales)[vec] = s;
+      if (l == 0) (p.is_v ? a.v_scales : a.k_scales)[vec] = s;
     }
   }
 }
@@ -135,8 +179,8 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(const KvArgs a, const Kv
 template <int D, int BITS, bool F32>
 __global__ void __launch_bounds__(kThreads) k_kv_read(const KvArgs a, const KvDense y, int tile, float norm) {
   constexpr int LPV = KvLanes<D>::LPV;
-  constexpr float MAGIC = 8388608.0f + float(1 << (BITS - 1));
   __shared__ Tile tl;
+  __shared__ __align__(16) float factors[2][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
   const int64_t t0 = int64_t(blockIdx.x) * tile;
   const int nt = int(min(int64_t(tile), a.tokens - t0));
@@ -144,6 +188,8 @@ __global__ void __launch_bounds__(kThreads) k_kv_read(const KvArgs a, const KvDe
     const KvToken k = kv_token(a, t0 + j, lane);
     if (lane == 0) tl.tok[j] = k;
   }
+  kv_factors<D>(factors[0], a.k_signs, norm);
+  kv_factors<D>(factors[1], a.v_signs, norm);
   __syncthreads();
   const int l = threadIdx.x % LPV;
   const int vectors = nt * 2 * a.hk;
@@ -158,13 +204,11 @@ __global__ void __launch_bounds__(kThreads) k_kv_read(const KvArgs a, const KvDe
     void* dst = const_cast<void*>(is_v ? y.v : y.k);
     const bool owned = in && dst != nullptr && tl.tok[j].seq >= 0;
     const int64_t slot = tl.tok[j].slot;
-    float z[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) z[i] = 0.0f;
+    float z[32], s = 0.0f;
     if (owned && slot >= 0) {
       const int64_t vec = slot + (int64_t(h) << a.log_page);
       const uint8_t* src = (is_v ? a.v_codes : a.k_codes) + vec * (D * BITS / 8);
-      const float s = (is_v ? a.v_scales : a.k_scales)[vec] * norm;
+      s = (is_v ? a.v_scales : a.k_scales)[vec];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         uint32_t w[2];
@@ -174,14 +218,17 @@ __global__ void __launch_bounds__(kThreads) k_kv_read(const KvArgs a, const KvDe
           const uint2 t = reinterpret_cast<const uint2*>(src)[c * LPV + l];
           w[0] = t.x, w[1] = t.y;
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          z[8 * c + e] = (__uint_as_float(0x4B000000u | code_at<BITS>(w, e)) - MAGIC) * s;
+        kv_dequantize<BITS>(w, z + 8 * c);
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) z[i] = 0.0f;
     }
-    kv_hadamard<D>(z, l);
+    kv_hadamard<D>(z, l);  // of whole numbers: exact
     if (owned) {
-      kv_signs<D>(z, is_v ? a.v_signs : a.k_signs, l);
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) mul_x2(z[i], z[i + 1], s, s);
+      kv_times<D>(z, factors[is_v], l);
       const int64_t at = (t0 + j) * (is_v ? y.v_ts : y.k_ts) + h * (is_v ? y.v_hs : y.k_hs);
 #pragma unroll
       for (int c = 0; c < 4; ++c) kv_store8<F32>(dst, at + 8 * (c * LPV + l), z + 8 * c);
@@ -189,11 +236,19 @@ __global__ void __launch_bounds__(kThreads) k_kv_read(const KvArgs a, const KvDe
   }
 }
 
-// Tokens per CTA: one while the tokens do not fill the GPU twice, more after
-// that (angles and places of neighbouring tokens are then found together).
-int pick_tile(int64_t tokens) {
-  const int64_t per = tokens / (2 * 148);
-  return int(std::min<int64_t>(kMaxTile, std::max<int64_t>(1, per)));
+// Tokens per CTA: one while the tokens do not fill the GPU twice; else the
+// smallest number whose vectors fill the CTA's passes to nine tenths.
+int pick_tile(int64_t tokens, int hk, int lpv) {
+  const int per = kThreads / lpv;
+  int best = 1;
+  double use = 0.0;
+  for (int t = 1; t <= kMaxTile && (t == 1 || tokens / t >= 2 * 148); ++t) {
+    const int v = 2 * hk * t;
+    const double u = double(v) / ((v + per - 1) / per * per);
+    if (u > use + 0.05) use = u, best = t;
+    if (use >= 0.9) break;
+  }
+  return best;
 }
 int pick_threads(int tile, int hk, int lpv) {
   const int64_t want = int64_t(tile) * 2 * hk * lpv;
@@ -220,7 +275,7 @@ struct Append {
   cudaStream_t st;
   template <int D, int BITS, bool F32>
   cudaError_t go() {
-    const int tile = pick_tile(a.tokens);
+    const int tile = pick_tile(a.tokens, a.hk, D / 32);
     const unsigned grid = unsigned((a.tokens + tile - 1) / tile);
     const int threads = pick_threads(tile, a.hk, D / 32);
     k_kv_append<D, BITS, F32><<<grid, threads, size_t(tile) * a.n_freq * sizeof(float2), st>>>(a, x, tile, norm_of(D));
@@ -233,7 +288,7 @@ struct Read {
   cudaStream_t st;
   template <int D, int BITS, bool F32>
   cudaError_t go() {
-    const int tile = pick_tile(a.tokens);
+    const int tile = pick_tile(a.tokens, a.hk, D / 32);
     const unsigned grid = unsigned((a.tokens + tile - 1) / tile);
     k_kv_read<D, BITS, F32><<<grid, pick_threads(tile, a.hk, D / 32), 0, st>>>(a, y, tile, norm_of(D));
     return cudaGetLastError();
