@@ -70,6 +70,35 @@ __device__ __forceinline__ KvToken kv_token(const KvArgs& a, int64_t t, int lane
   return k;
 }
 
+// Tokens t0 + lane of the call, one to a lane (lanes from n on: none).
+__device__ __forceinline__ KvToken kv_tokens(const KvArgs& a, int64_t t0, int n, int lane) {
+  KvToken k{-1, 0, -1};
+  const int64_t t = t0 + lane;
+  int64_t b = 0, e = 0, len = 0;
+  int s = -1;
+  if (a.seqs < 32) {  // every boundary and length is some lane's: one round of loads
+    const int cu = lane <= a.seqs ? __ldg(a.cu + lane) : 0;
+    const int ln = lane < a.seqs ? __ldg(a.lens + lane) : 0;
+    int c = 0;
+    for (int i = 0; i <= a.seqs; ++i) c += __shfl_sync(0xffffffffu, cu, i) <= t;
+    s = c - 1;
+    b = __shfl_sync(0xffffffffu, cu, max(s, 0));
+    e = __shfl_sync(0xffffffffu, cu, min(c, 31));
+    len = __shfl_sync(0xffffffffu, ln, max(s, 0));
+    if (s >= a.seqs) s = -1;
+  } else {
+    s = kv_count_le(a.cu, a.seqs, t0, lane) - 1;  // of the first token; the others are a few sequences on
+    while (s < a.seqs && __ldg(a.cu + s + 1) <= t) ++s;
+    if (s >= a.seqs) s = -1;
+    if (s >= 0) b = __ldg(a.cu + s), e = __ldg(a.cu + s + 1), len = __ldg(a.lens + s);
+  }
+  if (lane >= n || s < 0 || t < b || t >= e) return k;
+  k.seq = s;
+  k.pos = len - (e - b) + (t - b);
+  k.slot = kv_slot(a, s, k.pos);
+  return k;
+}
+
 // Rotary angles.  A frequency is held as the fraction of a turn that one
 // position makes, in units of 2^-64: a position times it, modulo 2^64, is the
 // angle's fraction of a turn, exactly, in one integer product (in fp32 a

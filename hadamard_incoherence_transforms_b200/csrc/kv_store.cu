@@ -14,7 +14,8 @@ namespace hit {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTile = 8;  // tokens per CTA
+constexpr int kMaxTile = 64;  // tokens per CTA
+constexpr int kAppendCtas = 2, kReadCtas = 4;  // CTAs on an SM
 
 // max that keeps a NaN
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -95,7 +96,7 @@ struct Tile {
 // A CTA's tile of tokens; vector v of it is token v / (2 hk), keys of all heads
 // before values.
 template <int D, int BITS, bool F32>
-__global__ void __launch_bounds__(kThreads) k_kv_append(const KvArgs a, const KvDense x, int tile, float norm) {
+__global__ void __launch_bounds__(kThreads, kAppendCtas) k_kv_append(const KvArgs a, const KvDense x, int tile, float norm) {
   constexpr int LPV = KvLanes<D>::LPV;
   extern __shared__ __align__(16) float2 cs[];  // [tile][n_freq]
   __shared__ Tile tl;
@@ -119,25 +120,24 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(const KvArgs a, const Kv
     p.h = p.is_v ? r - a.hk : r;
     return p;
   };
-  float y[32];
+  // a vector's pieces as they lie in memory, 16 bytes each
+  constexpr int RAW = F32 ? 8 : 4;
+  uint4 raw[RAW];
   auto load = [&](const Place& p) {
     const void* src = p.is_v ? x.v : x.k;
     const int64_t at = (t0 + p.j) * (p.is_v ? x.v_ts : x.k_ts) + p.h * (p.is_v ? x.v_hs : x.k_hs);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      if (p.in) {
-        kv_load8<F32>(src, at + 8 * (c * LPV + l), y + 8 * c);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[8 * c + e] = 0.0f;
-      }
+    for (int c = 0; c < RAW; ++c) {
+      raw[c] = make_uint4(0, 0, 0, 0);
+      const int64_t e = at + (F32 ? 8 * ((c >> 1) * LPV + l) + 4 * (c & 1) : 8 * (c * LPV + l));
+      if (p.in) raw[c] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(src) + e * (F32 ? 4 : 2)));
     }
   };
   Place p = place(threadIdx.x / LPV);
   load(p);  // the first vectors are on their way while their places are found
-  for (int j = warp; j < nt; j += nw) {
-    const KvToken k = kv_token(a, t0 + j, lane);
-    if (lane == 0) tl.tok[j] = k;
+  for (int j = 32 * warp; j < nt; j += 32 * nw) {
+    const KvToken k = kv_tokens(a, t0 + j, nt - j, lane);
+    if (j + lane < nt) tl.tok[j + lane] = k;
   }
   kv_turns(a, turns, threadIdx.x, blockDim.x);
   kv_factors<D>(factors[0], a.k_signs, norm);
@@ -149,10 +149,21 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(const KvArgs a, const Kv
   }
   __syncthreads();
   for (int v0 = 0; v0 < vectors; v0 += per) {  // every lane stays in the loop for the shuffles
-    if (v0 > 0) {
-      p = place(v0 + int(threadIdx.x) / LPV);
-      load(p);
+    float y[32];
+#pragma unroll
+    for (int c = 0; c < RAW; ++c) {
+      if constexpr (F32) {
+        y[4 * c] = __uint_as_float(raw[c].x), y[4 * c + 1] = __uint_as_float(raw[c].y);
+        y[4 * c + 2] = __uint_as_float(raw[c].z), y[4 * c + 3] = __uint_as_float(raw[c].w);
+      } else {
+        bf16x2_to_f32(raw[c].x, y[8 * c], y[8 * c + 1]);
+        bf16x2_to_f32(raw[c].y, y[8 * c + 2], y[8 * c + 3]);
+        bf16x2_to_f32(raw[c].z, y[8 * c + 4], y[8 * c + 5]);
+        bf16x2_to_f32(raw[c].w, y[8 * c + 6], y[8 * c + 7]);
+      }
     }
+    const Place p = place(v0 + int(threadIdx.x) / LPV);
+    if (v0 + per < vectors) load(place(v0 + per + int(threadIdx.x) / LPV));  // the next vectors
     const int64_t slot = tl.tok[p.j].slot;
     const bool live = p.in && slot >= 0;
     if (live && !p.is_v && a.n_freq > 0)
@@ -177,16 +188,16 @@ __global__ void __launch_bounds__(kThreads) k_kv_append(const KvArgs a, const Kv
 }
 
 template <int D, int BITS, bool F32>
-__global__ void __launch_bounds__(kThreads) k_kv_read(const KvArgs a, const KvDense y, int tile, float norm) {
+__global__ void __launch_bounds__(kThreads, kReadCtas) k_kv_read(const KvArgs a, const KvDense y, int tile, float norm) {
   constexpr int LPV = KvLanes<D>::LPV;
   __shared__ Tile tl;
   __shared__ __align__(16) float factors[2][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
   const int64_t t0 = int64_t(blockIdx.x) * tile;
   const int nt = int(min(int64_t(tile), a.tokens - t0));
-  for (int j = warp; j < nt; j += nw) {
-    const KvToken k = kv_token(a, t0 + j, lane);
-    if (lane == 0) tl.tok[j] = k;
+  for (int j = 32 * warp; j < nt; j += 32 * nw) {
+    const KvToken k = kv_tokens(a, t0 + j, nt - j, lane);
+    if (j + lane < nt) tl.tok[j + lane] = k;
   }
   kv_factors<D>(factors[0], a.k_signs, norm);
   kv_factors<D>(factors[1], a.v_signs, norm);
@@ -194,61 +205,70 @@ __global__ void __launch_bounds__(kThreads) k_kv_read(const KvArgs a, const KvDe
   const int l = threadIdx.x % LPV;
   const int vectors = nt * 2 * a.hk;
   const int per = blockDim.x / LPV;
-  for (int v0 = 0; v0 < vectors; v0 += per) {
-    const int v = v0 + int(threadIdx.x) / LPV;
-    const bool in = v < vectors;
-    const int j = in ? v / (2 * a.hk) : 0;
-    const int r = in ? v - j * 2 * a.hk : 0;
-    const bool is_v = r >= a.hk;
-    const int h = is_v ? r - a.hk : r;
-    void* dst = const_cast<void*>(is_v ? y.v : y.k);
-    const bool owned = in && dst != nullptr && tl.tok[j].seq >= 0;
+  struct Row {
+    int64_t at;
+    void* dst;  // NULL: not to be written
+    bool is_v, there;
+  };
+  uint32_t w[BITS];  // the lane's codes
+  float s = 0.0f;
+  auto load = [&](int v) {
+    Row r{0, nullptr, false, false};
+    s = 0.0f;
+    if (v >= vectors) return r;
+    const int j = v / (2 * a.hk), i = v - j * 2 * a.hk;
+    r.is_v = i >= a.hk;
+    const int h = r.is_v ? i - a.hk : i;
+    void* const dst = const_cast<void*>(r.is_v ? y.v : y.k);
+    if (tl.tok[j].seq < 0 || dst == nullptr) return r;
+    r.dst = dst;
+    r.at = (t0 + j) * (r.is_v ? y.v_ts : y.k_ts) + h * (r.is_v ? y.v_hs : y.k_hs);
     const int64_t slot = tl.tok[j].slot;
-    float z[32], s = 0.0f;
-    if (owned && slot >= 0) {
-      const int64_t vec = slot + (int64_t(h) << a.log_page);
-      const uint8_t* src = (is_v ? a.v_codes : a.k_codes) + vec * (D * BITS / 8);
-      s = (is_v ? a.v_scales : a.k_scales)[vec];
+    if (slot < 0) return r;
+    r.there = true;
+    const int64_t vec = slot + (int64_t(h) << a.log_page);
+    const uint8_t* src = (r.is_v ? a.v_codes : a.k_codes) + vec * (D * BITS / 8);
+    s = __ldg((r.is_v ? a.v_scales : a.k_scales) + vec);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t w[2];
-        if constexpr (BITS == 4) {
-          w[0] = reinterpret_cast<const uint32_t*>(src)[c * LPV + l];
-        } else {
-          const uint2 t = reinterpret_cast<const uint2*>(src)[c * LPV + l];
-          w[0] = t.x, w[1] = t.y;
-        }
-        kv_dequantize<BITS>(w, z + 8 * c);
+    for (int c = 0; c < 4; ++c) {
+      if constexpr (BITS == 4) {
+        w[c] = __ldg(reinterpret_cast<const uint32_t*>(src) + c * LPV + l);
+      } else {
+        const uint2 t = __ldg(reinterpret_cast<const uint2*>(src) + c * LPV + l);
+        w[2 * c] = t.x, w[2 * c + 1] = t.y;
       }
-    } else {
+    }
+    return r;
+  };
+  Row next = load(threadIdx.x / LPV);
+  for (int v0 = 0; v0 < vectors; v0 += per) {
+    const Row row = next;
+    const float scale = s;
+    float z[32];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) kv_dequantize<BITS>(w + c * (BITS / 4), z + 8 * c);
+    if (!row.there) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) z[i] = 0.0f;
     }
+    if (v0 + per < vectors) next = load(v0 + per + int(threadIdx.x) / LPV);  // the next codes
     kv_hadamard<D>(z, l);  // of whole numbers: exact
-    if (owned) {
+    if (row.dst != nullptr) {
 #pragma unroll
-      for (int i = 0; i < 32; i += 2) mul_x2(z[i], z[i + 1], s, s);
-      kv_times<D>(z, factors[is_v], l);
-      const int64_t at = (t0 + j) * (is_v ? y.v_ts : y.k_ts) + h * (is_v ? y.v_hs : y.k_hs);
+      for (int i = 0; i < 32; i += 2) mul_x2(z[i], z[i + 1], scale, scale);
+      kv_times<D>(z, factors[row.is_v], l);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) kv_store8<F32>(dst, at + 8 * (c * LPV + l), z + 8 * c);
+      for (int c = 0; c < 4; ++c) kv_store8<F32>(row.dst, row.at + 8 * (c * LPV + l), z + 8 * c);
     }
   }
 }
 
-// Tokens per CTA: one while the tokens do not fill the GPU twice; else the
-// smallest number whose vectors fill the CTA's passes to nine tenths.
-int pick_tile(int64_t tokens, int hk, int lpv) {
-  const int per = kThreads / lpv;
-  int best = 1;
-  double use = 0.0;
-  for (int t = 1; t <= kMaxTile && (t == 1 || tokens / t >= 2 * 148); ++t) {
-    const int v = 2 * hk * t;
-    const double u = double(v) / ((v + per - 1) / per * per);
-    if (u > use + 0.05) use = u, best = t;
-    if (use >= 0.9) break;
-  }
-  return best;
+// Tokens per CTA such that the CTAs that fit the GPU at once (`ctas` on an SM)
+// share them evenly: a CTA finds its tokens' places once and then has the next
+// vectors on their way while it works on these.
+int pick_tile(int64_t tokens, int ctas, int most) {
+  const int64_t at_once = 148 * ctas;
+  return int(std::max<int64_t>(1, std::min<int64_t>(most, (tokens + at_once - 1) / at_once)));
 }
 int pick_threads(int tile, int hk, int lpv) {
   const int64_t want = int64_t(tile) * 2 * hk * lpv;
@@ -275,7 +295,7 @@ struct Append {
   cudaStream_t st;
   template <int D, int BITS, bool F32>
   cudaError_t go() {
-    const int tile = pick_tile(a.tokens, a.hk, D / 32);
+    const int tile = pick_tile(a.tokens, kAppendCtas, D == 256 ? 32 : kMaxTile);  // at most 32 KB of angles
     const unsigned grid = unsigned((a.tokens + tile - 1) / tile);
     const int threads = pick_threads(tile, a.hk, D / 32);
     k_kv_append<D, BITS, F32><<<grid, threads, size_t(tile) * a.n_freq * sizeof(float2), st>>>(a, x, tile, norm_of(D));
@@ -288,7 +308,7 @@ struct Read {
   cudaStream_t st;
   template <int D, int BITS, bool F32>
   cudaError_t go() {
-    const int tile = pick_tile(a.tokens, a.hk, D / 32);
+    const int tile = pick_tile(a.tokens, kReadCtas, kMaxTile);
     const unsigned grid = unsigned((a.tokens + tile - 1) / tile);
     k_kv_read<D, BITS, F32><<<grid, pick_threads(tile, a.hk, D / 32), 0, st>>>(a, y, tile, norm_of(D));
     return cudaGetLastError();
