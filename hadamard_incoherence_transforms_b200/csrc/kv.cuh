@@ -172,10 +172,12 @@ __device__ __forceinline__ void kv_signs(float (&x)[32], const int8_t* __restric
   }
 }
 
-// Table of signs times `norm` for the elements of a head, by the whole CTA.
-template <int D>
+// Table of signs times `norm` for the elements of a head, by the whole CTA, with
+// PAD floats between its quarters.
+template <int D, int PAD>
 __device__ __forceinline__ void kv_factors(float* f, const int8_t* __restrict__ signs, float norm) {
-  for (int i = threadIdx.x; i < D; i += blockDim.x) f[i] = signs != nullptr && __ldg(signs + i) < 0 ? -norm : norm;
+  for (int i = threadIdx.x; i < D; i += blockDim.x)
+    f[i + i / (D / 4) * PAD] = signs != nullptr && __ldg(signs + i) < 0 ? -norm : norm;
 }
 // x <- x * f elementwise, f a table of the head's elements.
 template <int D>

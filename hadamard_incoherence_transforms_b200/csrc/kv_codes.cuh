@@ -60,4 +60,12 @@ __device__ __forceinline__ void bf_of8(uint32_t x, uint32_t& b0, uint32_t& b1) {
   b1 = badd2(bfma2(h1, 0x41804180u, 0xc510c510u), l1);
 }
 
+// d += A B for 16 x 8 x 16, fp16 operands.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 }  // namespace hit

@@ -7,6 +7,8 @@
 // and latency for short ones.  A vector sits on d / 32 lanes (32 elements
 // each), which leaves only 1 to 3 of the 6 to 8 Hadamard stages to shuffles.
 #include "kv.cuh"
+#include "internal.h"
+#include "kv_codes.cuh"
 
 #include <algorithm>
 
@@ -15,7 +17,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxTile = 64;  // tokens per CTA
-constexpr int kAppendCtas = 2, kReadCtas = 4;  // CTAs on an SM
+constexpr int kAppendCtas = 2, kReadCtas = 2;  // CTAs on an SM
 
 // max that keeps a NaN
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -72,37 +74,35 @@ __device__ __forceinline__ float kv_quantize(float (&x)[32], uint32_t (&w)[BITS]
   return s;
 }
 
-// Codes of eight elements (4 or 8 bytes) as fp32: the byte under 2^23's exponent,
-// minus 2^23 and the offset, exact.
-template <int BITS>
-__device__ __forceinline__ void kv_dequantize(const uint32_t* w, float* z) {
-  constexpr float OFF = -(8388608.0f + float(1 << (BITS - 1)));
-  const uint32_t a = BITS == 4 ? w[0] & 0x0f0f0f0fu : w[0], b = BITS == 4 ? (w[0] >> 4) & 0x0f0f0f0fu : w[1];
-#pragma unroll
-  for (int e = 0; e < 8; e += 2) {
-    // 4 bits: a holds the even elements, b the odd ones; 8 bits: a the first four
-    const uint32_t w0 = BITS == 4 ? a : e < 4 ? a : b, w1 = BITS == 4 ? b : w0;
-    const int i0 = BITS == 4 ? e / 2 : e % 4, i1 = BITS == 4 ? e / 2 : e % 4 + 1;
-    float x0 = __uint_as_float(__byte_perm(w0, 0x4b000000u, 0x7650 | i0));
-    float x1 = __uint_as_float(__byte_perm(w1, 0x4b000000u, 0x7650 | i1));
-    fma_x2(x0, x1, 1.0f, 1.0f, OFF, OFF, z[e], z[e + 1]);
-  }
-}
-
+// Places of a tile's tokens: slots (kv.cuh), kNone for a token of no sequence.
+constexpr int64_t kNone = -2;
 struct Tile {
-  KvToken tok[kMaxTile];
+  int64_t slot[kMaxTile];
+  int pos[kMaxTile];
+  __device__ __forceinline__ void find(const KvArgs& a, int64_t t0, int nt) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int j = 32 * warp; j < nt; j += 32 * int(blockDim.x >> 5)) {
+      const KvToken k = kv_tokens(a, t0 + j, nt - j, lane);
+      if (j + lane < nt) {
+        slot[j + lane] = k.seq < 0 ? kNone : k.slot;
+        pos[j + lane] = int(k.pos);
+      }
+    }
+  }
 };
+// n / d for n < 2^31 (make_fastdiv)
+__device__ __forceinline__ int div_by(int n, const FastDiv& f) { return int((__umulhi(uint32_t(n), f.mul) + uint32_t(n)) >> f.shr); }
 
 // A CTA's tile of tokens; vector v of it is token v / (2 hk), keys of all heads
 // before values.
 template <int D, int BITS, bool F32>
-__global__ void __launch_bounds__(kThreads, kAppendCtas) k_kv_append(const KvArgs a, const KvDense x, int tile, float norm) {
+__global__ void __launch_bounds__(kThreads, kAppendCtas) k_kv_append(const KvArgs a, const KvDense x, int tile, float norm,
+                                                                     FastDiv by_token) {
   constexpr int LPV = KvLanes<D>::LPV;
   extern __shared__ __align__(16) float2 cs[];  // [tile][n_freq]
   __shared__ Tile tl;
   __shared__ uint64_t turns[D / 2];
   __shared__ __align__(16) float factors[2][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
   const int64_t t0 = int64_t(blockIdx.x) * tile;
   const int nt = int(min(int64_t(tile), a.tokens - t0));
   const int l = threadIdx.x % LPV;
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) k_kv_append(const KvArg
   auto place = [&](int v) {
     Place p;
     p.in = v < vectors;
-    p.j = p.in ? v / (2 * a.hk) : 0;
+    p.j = p.in ? div_by(v, by_token) : 0;
     const int r = p.in ? v - p.j * 2 * a.hk : 0;
     p.is_v = r >= a.hk;
     p.h = p.is_v ? r - a.hk : r;
@@ -135,17 +135,14 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) k_kv_append(const KvArg
   };
   Place p = place(threadIdx.x / LPV);
   load(p);  // the first vectors are on their way while their places are found
-  for (int j = 32 * warp; j < nt; j += 32 * nw) {
-    const KvToken k = kv_tokens(a, t0 + j, nt - j, lane);
-    if (j + lane < nt) tl.tok[j + lane] = k;
-  }
+  tl.find(a, t0, nt);
   kv_turns(a, turns, threadIdx.x, blockDim.x);
-  kv_factors<D>(factors[0], a.k_signs, norm);
-  kv_factors<D>(factors[1], a.v_signs, norm);
+  kv_factors<D, 0>(factors[0], a.k_signs, norm);
+  kv_factors<D, 0>(factors[1], a.v_signs, norm);
   __syncthreads();
   for (int i = threadIdx.x; i < nt * a.n_freq; i += blockDim.x) {
     const int j = i / a.n_freq, f = i - j * a.n_freq;
-    if (tl.tok[j].slot >= 0) cs[i] = kv_angle(a, turns, t0 + j, int(tl.tok[j].pos), f);
+    if (tl.slot[j] >= 0) cs[i] = kv_angle(a, turns, t0 + j, tl.pos[j], f);
   }
   __syncthreads();
   for (int v0 = 0; v0 < vectors; v0 += per) {  // every lane stays in the loop for the shuffles
@@ -164,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) k_kv_append(const KvArg
     }
     const Place p = place(v0 + int(threadIdx.x) / LPV);
     if (v0 + per < vectors) load(place(v0 + per + int(threadIdx.x) / LPV));  // the next vectors
-    const int64_t slot = tl.tok[p.j].slot;
+    const int64_t slot = tl.slot[p.j];
     const bool live = p.in && slot >= 0;
     if (live && !p.is_v && a.n_freq > 0)
       kv_rope<D, F32>(y, x.k, (t0 + p.j) * x.k_ts + p.h * x.k_hs, cs + p.j * a.n_freq, a.n_freq, a.interleaved, l);
@@ -187,78 +184,165 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) k_kv_append(const KvArg
   }
 }
 
+// Read.  The transform of stored codes is a sum of whole numbers, exact in fp16
+// and on the tensor cores, so that it takes no shuffles: a warp takes 16 vectors,
+// lane (r, c) the codes of quarter c of vectors r and r + 8.  Of the log2 D element
+// bits the quarter's own ones but two are butterflies on fp16 pairs in registers;
+// the other two and the quarter's number are the 16 of m16n8k16's inner
+// dimension, against a +-1 matrix that lies in four registers.  Its columns are
+// numbered such that a lane ends with D / 4 neighbouring elements of its rows.
 template <int D, int BITS, bool F32>
-__global__ void __launch_bounds__(kThreads, kReadCtas) k_kv_read(const KvArgs a, const KvDense y, int tile, float norm) {
-  constexpr int LPV = KvLanes<D>::LPV;
+__global__ void __launch_bounds__(kThreads, kReadCtas) k_kv_read(const KvArgs a, const KvDense y, int tile, float norm,
+                                                                 int wide, FastDiv by_heads) {
+  constexpr int VB = D * BITS / 8, NW = VB / 16;  // a lane's words of a vector's codes
+  constexpr int NP = D / 8;                       // ... and its fp16 pairs
   __shared__ Tile tl;
-  __shared__ __align__(16) float factors[2][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  __shared__ __align__(16) float factors[2][D + 16];  // quarters in different banks
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r8 = lane >> 2, c4 = lane & 3;
   const int64_t t0 = int64_t(blockIdx.x) * tile;
   const int nt = int(min(int64_t(tile), a.tokens - t0));
-  for (int j = 32 * warp; j < nt; j += 32 * nw) {
-    const KvToken k = kv_tokens(a, t0 + j, nt - j, lane);
-    if (j + lane < nt) tl.tok[j + lane] = k;
+  tl.find(a, t0, nt);
+  kv_factors<D, 4>(factors[0], a.k_signs, norm);
+  kv_factors<D, 4>(factors[1], a.v_signs, norm);
+  // the +-1 matrix: inner index (quarter c, then the pair's half and which of two
+  // pairs), column 2 c' + u of tile t: c' is the output's quarter, u and t its bits
+  // for the pair's number and half (4 bits), or the other way around (8 bits)
+  uint32_t hm[2][2];
+  {
+    const int n = lane >> 2, s0 = __popc(c4 & (n >> 1)) & 1, u = n & 1;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int half = BITS == 4 ? t : u, pair = BITS == 4 ? u : t;
+      auto one = [&](int h, int p) { return 0x3c00u | (uint32_t((s0 + (h & half) + (p & pair)) & 1) << 15); };
+      hm[t][0] = one(0, 0) | (one(1, 0) << 16);
+      hm[t][1] = one(0, 1) | (one(1, 1) << 16);
+    }
   }
-  kv_factors<D>(factors[0], a.k_signs, norm);
-  kv_factors<D>(factors[1], a.v_signs, norm);
   __syncthreads();
-  const int l = threadIdx.x % LPV;
-  const int vectors = nt * 2 * a.hk;
-  const int per = blockDim.x / LPV;
+  const int vectors = nt * a.hk, groups = (vectors + 15) / 16;  // of keys; as many of values
   struct Row {
     int64_t at;
-    void* dst;  // NULL: not to be written
-    bool is_v, there;
+    bool owned;
   };
-  uint32_t w[BITS];  // the lane's codes
-  float s = 0.0f;
-  auto load = [&](int v) {
-    Row r{0, nullptr, false, false};
-    s = 0.0f;
-    if (v >= vectors) return r;
-    const int j = v / (2 * a.hk), i = v - j * 2 * a.hk;
-    r.is_v = i >= a.hk;
-    const int h = r.is_v ? i - a.hk : i;
-    void* const dst = const_cast<void*>(r.is_v ? y.v : y.k);
-    if (tl.tok[j].seq < 0 || dst == nullptr) return r;
-    r.dst = dst;
-    r.at = (t0 + j) * (r.is_v ? y.v_ts : y.k_ts) + h * (r.is_v ? y.v_hs : y.k_hs);
-    const int64_t slot = tl.tok[j].slot;
-    if (slot < 0) return r;
-    r.there = true;
-    const int64_t vec = slot + (int64_t(h) << a.log_page);
-    const uint8_t* src = (r.is_v ? a.v_codes : a.k_codes) + vec * (D * BITS / 8);
-    s = __ldg((r.is_v ? a.v_scales : a.k_scales) + vec);
+  uint32_t code[2][NW];
+  float scale[2];  // 0 for a position that does not exist: zeros, whatever the last codes were
+  auto load = [&](int g, Row (&row)[2]) {
+    const bool is_v = g >= groups;
+    const bool wanted = (is_v ? y.v : y.k) != nullptr;
+    const int64_t ts = is_v ? y.v_ts : y.k_ts, hs = is_v ? y.v_hs : y.k_hs;
+    const uint8_t* const codes = (is_v ? a.v_codes : a.k_codes) + c4 * (VB / 4);
+    const float* const scales = is_v ? a.v_scales : a.k_scales;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      if constexpr (BITS == 4) {
-        w[c] = __ldg(reinterpret_cast<const uint32_t*>(src) + c * LPV + l);
+    for (int k = 0; k < 2; ++k) {
+      const int v = (g - (is_v ? groups : 0)) * 16 + r8 + 8 * k;
+      row[k] = Row{0, false};
+      scale[k] = 0.0f;
+      if (v >= vectors || !wanted) continue;
+      const int j = div_by(v, by_heads), h = v - j * a.hk;
+      const int64_t slot = tl.slot[j];
+      row[k].owned = slot != kNone;
+      row[k].at = (t0 + j) * ts + h * hs + c4 * (D / 4);
+      if (slot < 0) continue;
+      const int64_t vec = slot + (int64_t(h) << a.log_page);
+      const uint8_t* src = codes + vec * VB;
+      scale[k] = __ldg(scales + vec);
+      if constexpr (NW == 2) {
+        const uint2 q = __ldg(reinterpret_cast<const uint2*>(src));
+        code[k][0] = q.x, code[k][1] = q.y;
       } else {
-        const uint2 t = __ldg(reinterpret_cast<const uint2*>(src) + c * LPV + l);
-        w[2 * c] = t.x, w[2 * c + 1] = t.y;
+#pragma unroll
+        for (int i = 0; i < NW; i += 4) {
+          const uint4 q = __ldg(reinterpret_cast<const uint4*>(src) + i / 4);
+          code[k][i] = q.x, code[k][i + 1] = q.y, code[k][i + 2] = q.z, code[k][i + 3] = q.w;
+        }
       }
     }
-    return r;
   };
-  Row next = load(threadIdx.x / LPV);
-  for (int v0 = 0; v0 < vectors; v0 += per) {
-    const Row row = next;
-    const float scale = s;
-    float z[32];
+  const int step = int(blockDim.x >> 5);
+  Row next[2];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) kv_dequantize<BITS>(w + c * (BITS / 4), z + 8 * c);
-    if (!row.there) {
+  for (int i = 0; i < NW; ++i) code[0][i] = code[1][i] = 0;
+  if (warp < 2 * groups) load(warp, next);
+  for (int g = warp; g < 2 * groups; g += step) {
+    const Row row[2] = {next[0], next[1]};
+    const float s[2] = {scale[0], scale[1]};
+    uint32_t p[2][NP];  // pairs: 4 bits (e, e + 4), e = 0 .. 3 of each eight; 8 bits (e, e + 1)
 #pragma unroll
-      for (int i = 0; i < 32; ++i) z[i] = 0.0f;
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        if constexpr (BITS == 4) {
+          uint32_t h[4];
+          half_of4(code[k][i], h);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) p[k][4 * i + e] = h[e];
+        } else {
+          half_of8(code[k][i], p[k][2 * i], p[k][2 * i + 1]);
+        }
+      }
+#pragma unroll
+      for (int b = 2; b < NP; b <<= 1) {  // butterflies on every bit of the pair's number but the lowest
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          if (i & b) continue;
+          const uint32_t u = p[k][i], w = p[k][i | b];
+          p[k][i] = hadd2(u, w);
+          p[k][i | b] = hadd2(u, w ^ 0x80008000u);
+        }
+      }
     }
-    if (v0 + per < vectors) next = load(v0 + per + int(threadIdx.x) / LPV);  // the next codes
-    kv_hadamard<D>(z, l);  // of whole numbers: exact
-    if (row.dst != nullptr) {
+    if (g + step < 2 * groups) load(g + step, next);  // the next codes
+    const bool is_v = g >= groups;
+    void* const dst = const_cast<void*>(is_v ? y.v : y.k);
+    const float* f = factors[is_v] + c4 * (D / 4 + 4);
 #pragma unroll
-      for (int i = 0; i < 32; i += 2) mul_x2(z[i], z[i + 1], scale, scale);
-      kv_times<D>(z, factors[row.is_v], l);
+    for (int e0 = 0; e0 < D / 4; e0 += 16) {  // sixteen elements of both rows
+      float z[2][16];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) kv_store8<F32>(row.dst, row.at + 8 * (c * LPV + l), z + 8 * c);
+      for (int m = 0; m < 4; ++m) {
+        const int i = e0 / 2 + 2 * m;  // pairs i, i + 1
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          mma_f16(d, p[0][i], p[1][i], p[0][i + 1], p[1][i + 1], hm[t][0], hm[t][1]);
+          // element of (pair number without its lowest bit, tile, column's low bit)
+          const int e = BITS == 4 ? 8 * (m >> 1) + 2 * (m & 1) + 4 * t : 4 * m + 2 * t;
+          z[0][e] = d[0], z[0][e + 1] = d[1];
+          z[1][e] = d[2], z[1][e + 1] = d[3];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (!row[k].owned) continue;
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+          const float4 q = *reinterpret_cast<const float4*>(f + e0 + e);
+          float* w = z[k] + e;
+          mul_x2(w[0], w[1], s[k], s[k]);
+          mul_x2(w[2], w[3], s[k], s[k]);
+          mul_x2(w[0], w[1], q.x, q.y);
+          mul_x2(w[2], w[3], q.z, q.w);
+        }
+        const float* w = z[k];
+        if (wide) {  // whole 32-byte sectors
+          if constexpr (F32) {
+            float* o = static_cast<float*>(dst) + row[k].at + e0;
+#pragma unroll
+            for (int e = 0; e < 16; e += 8)
+              st_stream_v8(o + e, __float_as_uint(w[e]), __float_as_uint(w[e + 1]), __float_as_uint(w[e + 2]),
+                           __float_as_uint(w[e + 3]), __float_as_uint(w[e + 4]), __float_as_uint(w[e + 5]),
+                           __float_as_uint(w[e + 6]), __float_as_uint(w[e + 7]));
+          } else {
+            st_stream_v8(static_cast<__nv_bfloat16*>(dst) + row[k].at + e0, f32_to_bf16x2(w[0], w[1]),
+                         f32_to_bf16x2(w[2], w[3]), f32_to_bf16x2(w[4], w[5]), f32_to_bf16x2(w[6], w[7]),
+                         f32_to_bf16x2(w[8], w[9]), f32_to_bf16x2(w[10], w[11]), f32_to_bf16x2(w[12], w[13]),
+                         f32_to_bf16x2(w[14], w[15]));
+          }
+        } else {
+          kv_store8<F32>(dst, row[k].at + e0, w);
+          kv_store8<F32>(dst, row[k].at + e0 + 8, w + 8);
+        }
+      }
     }
   }
 }
@@ -298,7 +382,8 @@ struct Append {
     const int tile = pick_tile(a.tokens, kAppendCtas, D == 256 ? 32 : kMaxTile);  // at most 32 KB of angles
     const unsigned grid = unsigned((a.tokens + tile - 1) / tile);
     const int threads = pick_threads(tile, a.hk, D / 32);
-    k_kv_append<D, BITS, F32><<<grid, threads, size_t(tile) * a.n_freq * sizeof(float2), st>>>(a, x, tile, norm_of(D));
+    k_kv_append<D, BITS, F32><<<grid, threads, size_t(tile) * a.n_freq * sizeof(float2), st>>>(a, x, tile, norm_of(D),
+                                                                                                 make_fastdiv(2 * a.hk));
     return cudaGetLastError();
   }
 };
@@ -310,7 +395,13 @@ struct Read {
   cudaError_t go() {
     const int tile = pick_tile(a.tokens, kReadCtas, kMaxTile);
     const unsigned grid = unsigned((a.tokens + tile - 1) / tile);
-    k_kv_read<D, BITS, F32><<<grid, pick_threads(tile, a.hk, D / 32), 0, st>>>(a, y, tile, norm_of(D));
+    // a warp for each 16 vectors of either kind, eight at most
+    const int64_t groups = 2 * ((int64_t(tile) * a.hk + 15) / 16);
+    const int threads = 32 * int(std::min<int64_t>(kThreads / 32, groups));
+    const int es = F32 ? 4 : 2;
+    const bool wide = (reinterpret_cast<uintptr_t>(y.k) | reinterpret_cast<uintptr_t>(y.v) | uintptr_t(y.k_ts * es) |
+                       uintptr_t(y.k_hs * es) | uintptr_t(y.v_ts * es) | uintptr_t(y.v_hs * es)) % 32 == 0;
+    k_kv_read<D, BITS, F32><<<grid, threads, 0, st>>>(a, y, tile, norm_of(D), wide, make_fastdiv(a.hk));
     return cudaGetLastError();
   }
 };
