@@ -157,21 +157,6 @@ __device__ __forceinline__ void kv_hadamard(float (&x)[32], int l) {
   for (int b = 0; b < KvLanes<D>::LOG; ++b) shfl_stage<32>(x, b, (l >> b) & 1);
 }
 
-// x <- diag(signs) x
-template <int D>
-__device__ __forceinline__ void kv_signs(float (&x)[32], const int8_t* __restrict__ signs, int l) {
-  if (signs == nullptr) return;
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const int q = c * KvLanes<D>::LPV + l;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t b = uint32_t(uint8_t(__ldg(signs + 8 * q + e)));
-      x[8 * c + e] = __uint_as_float(__float_as_uint(x[8 * c + e]) ^ ((b << 24) & 0x80000000u));
-    }
-  }
-}
-
 // Table of signs times `norm` for the elements of a head, by the whole CTA, with
 // PAD floats between its quarters.
 template <int D, int PAD>
@@ -203,18 +188,13 @@ __device__ __forceinline__ void kv_row_power(uint32_t m, float& up, float& down)
   up = odd ? 1.0f : __uint_as_float(ex << 23);
   down = odd ? 1.0f : __uint_as_float(ex == 254 ? 0x00400000u : (254 - ex) << 23);
 }
-// Unnormalised rotated query x to base-2 scores, and the power of two `up` of
-// the row's largest element with `down` = 1 / up: x * down is in [-2, 2), where
-// fp16 keeps it to half a step of 2^-10 of its largest element or better.
+// The same of a whole vector: x * down is in [-2, 2), where fp16 keeps it to half
+// a step of 2^-10 of its largest element or better.
 template <int D>
-__device__ __forceinline__ void kv_query_scale(float (&x)[32], float scale, float& up, float& down) {
-  const float f = (D == 64 ? 0.125f : D == 256 ? 0.0625f : 0.08838834764831845f) * 1.4426950408889634f * scale;
+__device__ __forceinline__ void kv_row_power(const float (&x)[32], float& up, float& down) {
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    x[i] *= f;
-    m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
-  }
+  for (int i = 0; i < 32; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
 #pragma unroll
   for (int b = 0; b < KvLanes<D>::LOG; ++b) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1 << b));
   kv_row_power(m, up, down);

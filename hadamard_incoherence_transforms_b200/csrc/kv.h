@@ -42,6 +42,7 @@ struct KvAttn {
   int64_t q_ts = 0, q_hs = 0, o_ts = 0, o_hs = 0;
   int heads = 0, group = 1;  // query heads; of one key/value head
   int q_f32 = 0, o_f32 = 0, causal = 1;
+  int wide = 0;  // every row of out starts on a 32-byte boundary
   int64_t rows_lo = 0, rows_hi = INT64_MAX;  // sequences with this many query rows (token * group) belong to the launch
   float scale = 1.0f;
   int64_t window = 0;

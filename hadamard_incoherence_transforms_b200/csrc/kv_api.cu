@@ -29,11 +29,12 @@ int cuda_status(cudaError_t e, const char* what) {
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 constexpr int64_t kMaxTokens = int64_t(1) << 31;
-constexpr int64_t kFewRows = 16;
+constexpr int64_t kFewRows = 64;
 
 // Sequences with up to kFewRows query rows for a key/value head go to the kernel
-// that streams the codes once for 16 rows, the others to the one that works on
-// 256 rows at a time.  Each launch leaves the other's sequences alone, so that
+// that streams the codes once for 16 rows (an SM takes 7 cycles for a position and
+// 16 rows), the others to the one that works on 256 rows at a time (40 cycles for a
+// position, whatever the rows).  Each launch leaves the other's sequences alone, so that
 // max_new decides only whether the second kind is needed.
 bool few_only(int64_t max_new, int64_t group, int head_dim) { return head_dim == 256 || max_new * group <= kFewRows; }
 
@@ -208,6 +209,8 @@ int rht_kv_attention(const hit_kv* kv, const void* q, void* out, int64_t tokens,
   t.group = heads / a.hk;
   t.q_f32 = dtype_q == HIT_F32;
   t.o_f32 = dtype_out == HIT_F32;
+  const int64_t out_bytes = t.o_f32 ? 4 : 2;
+  t.wide = aligned(out, 32) && o_ts * out_bytes % 32 == 0 && o_hs * out_bytes % 32 == 0;
   t.causal = causal ? 1 : 0;
   t.scale = sm_scale;
   t.window = window;

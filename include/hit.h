@@ -404,7 +404,7 @@ HIT_API int harp_blocks(const float* theta, const int8_t* theta_q, float theta_s
  *   only) only j > p - window.  A token that sees nothing gets 0.  q, out:
  *   [tokens, heads, head_dim], strided as k.  Arithmetic: queries (behind a
  *   power of two of their own row) fp16, scores and outputs summed in fp32,
- *   softmax in fp32, probabilities bf16.  Where a sequence has at most 16 query
+ *   softmax in fp32, probabilities bf16.  Where a sequence has at most 64 query
  *   rows (tokens * heads / kv_heads) for a key/value head, or head_dim is 256,
  *   codes and scales enter exactly; in longer chunks keys are rounded once to
  *   fp16 and values once to bf16, as an unquantized cache would hold them.
