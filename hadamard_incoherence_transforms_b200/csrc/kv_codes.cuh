@@ -1,6 +1,6 @@
-// Stored codes to matrix operands, in registers and without an error: fp16 for
-// keys, bf16 for values (the other operand of a value is a probability times a
-// scale, which spans more than fp16's range).
+// Stored codes to matrix operands, in registers and without an error: fp16, or
+// bf16 for values whose other operand is a probability times a scale, which spans
+// more than fp16's range.
 #pragma once
 #include <stdint.h>
 

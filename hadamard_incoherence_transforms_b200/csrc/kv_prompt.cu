@@ -5,17 +5,16 @@
 // head, 256 query rows) x 128 positions units.  Roles:
 //   warps 0-3, 4-7  softmax of the upper and of the lower 128 query rows, a
 //                   thread a row, its scores in tensor memory;
-//   warps 8-11      codes to fp16 keys and bf16 values in shared memory (128-byte
+//   warps 8-11      codes to fp16 keys and values in shared memory (128-byte
 //                   swizzle), a two-stage ring each, the next unit's codes on
 //                   their way in registers;
 //   warp 13         finds the CTA's segments and hands them to the others;
-//   warp 12         one thread issues the products: S = Q K^T (fp16), O += P V
-//                   (bf16, P read from tensor memory where it replaced S).
+//   warp 12         one thread issues the products: S = Q K^T, O += P V (fp16, P
+//                   read from tensor memory where it replaced S).
 // The two halves alternate: while one half's softmax runs, the tensor cores
 // work on the other's products.  Key and value units are converted once for
-// both, their scales folded in with one rounding (2^-11 of a key, 2^-8 of a
-// value: half the work of the softmax roles went into scales otherwise, see
-// UnitSoftmax for what is left of it).
+// both, their scales folded in with one rounding of 2^-11 (half the work of the
+// softmax roles went into scales otherwise, see UnitSoftmax for what is left).
 #include "internal.h"
 #include "kv_codes.cuh"
 #include "kv_split.cuh"
@@ -35,17 +34,19 @@ constexpr int kRows = 256;      // query rows of a unit
 constexpr int kKeys = 128;      // positions of a unit
 constexpr int kThreads = 16 * 32;  // warps 14 and 15 are idle: registers are dealt out to groups of four warps
 constexpr int kCtas = 148;
-constexpr float kGrow = 65536.0f;  // sum of 32 probabilities above which a row gets a new reference
+constexpr float kGrow = 32768.0f;  // sum of 32 probabilities above which a row gets a new reference
+constexpr float kRoom = 4.0f;      // a reference's own probability is 2^kRoom
+constexpr int kValueBits = 4;      // the largest scale of a segment's first unit becomes 2^kValueBits or more
 
 template <int D>
 struct Prompt {
   static constexpr int BLK = D / 64;             // 64-element column blocks of an operand
   static constexpr int TILE = BLK * 128 * 128;   // 128 vectors of D 16-bit elements
   static constexpr int Q = 0, K = 2 * TILE, V = 4 * TILE, SC = 6 * TILE;
-  // ring of four units: which positions exist (128 bits), the power of two of the key scales
+  // ring of four units: which positions exist (128 bits), the powers of two of the scales
   static constexpr int SC_STAGE = 32;
-  static constexpr int TS = SC + 4 * SC_STAGE;   // the largest key scale of each unpacking warp, two units
-  static constexpr int BARS = TS + 32;
+  static constexpr int TS = SC + 4 * SC_STAGE;   // the largest scales of each unpacking warp, two units
+  static constexpr int BARS = TS + 64;
   static constexpr int BYTES = BARS + 512 + 1024;
   static constexpr int S_COL = 0, O_COL = 2 * 128;  // tensor memory columns
   static constexpr int COLS = 512;
@@ -312,10 +313,9 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo, uint
   return uint64_t((addr >> 4) & 0x3fff) | (uint64_t((lbo >> 4) & 0x3fff) << 16) | (uint64_t((sbo >> 4) & 0x3fff) << 32) |
          (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
-// fp32 accumulator; A and B both fp16 or both bf16; A K-major, M = 128
-__host__ __device__ constexpr uint32_t instr_desc(bool bf16, int n, bool b_mn_major) {
-  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (uint32_t(b_mn_major) << 16) | (uint32_t(n >> 3) << 17) |
-         (uint32_t(128 >> 4) << 24);
+// fp32 accumulator; A and B fp16; A K-major, M = 128
+__host__ __device__ constexpr uint32_t instr_desc(int n, bool b_mn_major) {
+  return (1u << 4) | (uint32_t(b_mn_major) << 16) | (uint32_t(n >> 3) << 17) | (uint32_t(128 >> 4) << 24);
 }
 // Shared-memory descriptors as their two words.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t id, bool add) {
@@ -411,16 +411,17 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // One row's softmax of a unit: its 128 scores in tensor memory become
-// probabilities (bf16, in the same place).  m: the reference they are relative
+// probabilities (fp16, in the same place).  m: the reference they are relative
 // to, a maximum of scores seen before; l: the sum of probabilities; fix: what
 // sums from before have to be multiplied with.
 //
 // 32 columns at a time, stored as soon as they are done (holding all of them
 // costs more registers than the roles leave).  No maximum is taken as long as a
-// row's probabilities add up to less than kGrow: bf16 and fp32 hold a probability
-// of 2^16 as well as one of 1.  Above it, or while a row has no reference yet, the
-// largest score becomes the reference of the rows concerned, and the columns
-// already stored (and, through `fix`, l and O) are brought to it.
+// row's probabilities add up to less than kGrow, which fp16 holds.  Above it, or
+// while a row has no reference yet, the largest score, less kRoom, becomes the
+// reference of the rows concerned, and the columns already stored (and, through
+// `fix`, l and O) are brought to it.  fp16 then keeps 11 bits of a probability down
+// to 2^-18 of the largest one, and the rest to 2^-29 of it.
 struct UnitSoftmax {
   uint32_t s_at, p_at;  // tensor memory of the scores and of the probabilities
   uint4 there;          // positions that exist
@@ -457,7 +458,7 @@ struct UnitSoftmax {
     };
     auto finish = [&](int g, int h, const float (&y)[4]) {
       asm volatile("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[h]) : "l"(pk2(y[2 * h], y[2 * h + 1])));
-      asm volatile("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[2 * g + h]) : "f"(y[2 * h + 1]), "f"(y[2 * h]));
+      asm volatile("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(p[2 * g + h]) : "f"(y[2 * h + 1]), "f"(y[2 * h]));
     };
     auto power = [](float y) {
       float r;
@@ -497,8 +498,8 @@ struct UnitSoftmax {
     for (int i = 0; i < 32; ++i) top = (see >> i) & 1 ? fmaxf(top, __uint_as_float(w[i])) : top;
     top *= qu;
     const bool grow = m == -INFINITY ? top > m : sum > kGrow;
-    const float f = grow ? ex2(m - top) : 1.0f;  // 0 for a first reference
-    if (grow) m = top;
+    const float f = grow ? ex2(m - (top - kRoom)) : 1.0f;  // 0 for a first reference
+    if (grow) m = top - kRoom;
     const float base = m == -INFINITY ? 0.0f : -m;
     base2 = pk2(base, base);
     fix *= f;
@@ -510,9 +511,9 @@ struct UnitSoftmax {
       tmem_load16_now(p_at + 16 * k, p);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        float y0, y1;
-        bf16x2_to_f32(p[i], y0, y1);
-        p[i] = f32_to_bf16x2(y0 * f, y1 * f);
+        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&p[i]));
+        const __half2 z = __floats2half2_rn(y.x * f, y.y * f);
+        p[i] = *reinterpret_cast<const uint32_t*>(&z);
       }
       tmem_store16(p_at + 16 * k, p);
     }
@@ -567,7 +568,7 @@ struct UnitSoftmax {
 // the order in which the codes fall out of a word.
 template <int BITS>
 __host__ __device__ constexpr int v_elem(int c) {
-  return BITS == 4 ? (c >> 1) + 4 * (c & 1) : (c & 4) + 2 * (c & 1) + ((c >> 1) & 1);
+  return BITS == 4 ? (c >> 1) + 4 * (c & 1) : c;
 }
 
 // ---------------------------------------------------------------------------
@@ -741,6 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
       const int tok = mine ? row / t.group : 0;
       const int head = g.h * t.group + (mine ? row - tok * t.group : 0);
       float m = -INFINITY, l = 0.0f;
+      uint32_t ve = 0;  // exponent of the power of two that O is relative to
       bool ok = true;
       if (f.js < f.je) {
         // the half's queries, a row's 16-byte pieces to their swizzled places
@@ -774,6 +776,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
           ++ns;
           fence_after();
           const uint4 there = *reinterpret_cast<const uint4*>(scp);
+          const uint32_t ve_before = j > f.js ? ve : 0;
+          ve = *reinterpret_cast<const uint32_t*>(scp + 20);
           const float qu = qe * *reinterpret_cast<const float*>(scp + 16);
           const int64_t p0 = int64_t(j) * kKeys;
           const bool full = p0 >= f.lo_max && p0 + kKeys <= f.hi_min && (there.x & there.y & there.z & there.w) == ~0u;
@@ -784,6 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
           const UnitSoftmax unit{s_at, s_at, there, c_lo, c_hi, qu};
           if (full) unit.run<true>(m, l, fix);
           else unit.run<false>(m, l, fix);
+          if (ve_before != 0 && ve != ve_before) fix *= __uint_as_float(uint32_t(max(0, 127 + int(ve_before) - int(ve))) << 23);
           if (j > f.js && __any_sync(0xffffffffu, fix != 1.0f)) {
             // the product of the unit before has to be in O
             ok = mbar_wait(&bars->o[hf], (no - 1) & 1u);
@@ -818,7 +823,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
       // ---------------- the half's result ----------------
       const bool any = f.js < f.je;
       const size_t slot_row = (2 * size_t(blockIdx.x) + (g.begins ? 1 : 0)) * kRows + 128 * hf + r;
-      const float inv = l == 0.0f ? 0.0f : (D == 64 ? 0.125f : 0.08838834764831845f) / l;
+      const float up = __uint_as_float(ve << 23);
+      const float inv = l == 0.0f ? 0.0f : (D == 64 ? 0.125f : 0.08838834764831845f) / l * up;
       if (f.rows > 0) {  // by the whole warp: tensor memory is read together
         if (g.whole) {
           constexpr int N = D / 64;  // the transform's last stage joins the halves of 128 elements
@@ -872,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
             if (any) tmem_load32_now(o_at + 32 * c, u);
             float x[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[8 * (i / 8) + v_elem<BITS>(i % 8)] = any ? __uint_as_float(u[i]) : 0.0f;
+            for (int i = 0; i < 32; ++i) x[8 * (i / 8) + v_elem<BITS>(i % 8)] = any ? __uint_as_float(u[i]) * up : 0.0f;
             if (mine) {
 #pragma unroll
               for (int i = 0; i < 32; i += 8) kv_store8<true>(work.rows, slot_row * D + 32 * c + i, x + i);
@@ -907,6 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
       const int32_t* const pages = a.table + int64_t(w.seg().s) * a.ld_table;
       uint4 kr[CH], vr[CH];
       float ksc = 0.0f, vsc = 0.0f;
+      int vex = 0;  // exponent of the largest value scale that the segment's values are relative to
       bool in = false;
       // the page of this thread's position in unit j (-1: there is none), and its vector in that page
       auto page_of = [&](int j) {
@@ -950,17 +957,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
         if (!ok) break;
         // The scales are folded into the operands, with one rounding: a product
         // with a scale in two parts, hi and the rest.  Keys are relative to a
-        // power of two of the unit's largest scale, so that fp16 holds them.  A
-        // position whose scale is not finite becomes NaN in its scores, and only there.
-        uint32_t* const tops = reinterpret_cast<uint32_t*>(smem + F::TS + (kv & 1) * 16);
+        // power of two of the unit's largest scale, so that fp16 holds them, values
+        // to one of the largest scale of the segment's first unit: a later unit
+        // whose scales are more than 2^3 times as large takes its own, and O is
+        // brought to it.  Codes times scales then stay below 2^15, and scales down to
+        // 2^-18 of the largest keep 11 bits (bf16 values cost the result 2^-8 of
+        // each, 0.0029 in place of 0.0017 in all).  A position whose scale is not
+        // finite becomes NaN in its scores, and only there.
+        uint32_t* const tops = reinterpret_cast<uint32_t*>(smem + F::TS + (kv & 1) * 32);
         uint8_t* const scp = smem + F::SC + (kv & 3) * F::SC_STAGE;
         const bool k_fine = (__float_as_uint(ksc) & 0x7f800000u) != 0x7f800000u;
         const bool v_fine = (__float_as_uint(vsc) & 0x7f800000u) != 0x7f800000u;
         {
           const uint32_t top = __reduce_max_sync(0xffffffffu, k_fine ? __float_as_uint(ksc) & 0x7fffffffu : 0u);
+          const uint32_t vtop = __reduce_max_sync(0xffffffffu, v_fine ? __float_as_uint(vsc) & 0x7fffffffu : 0u);
           const uint32_t b = __ballot_sync(0xffffffffu, in);
           if (lane == 0) {
             tops[warp - 8] = top;
+            tops[warp - 4] = vtop;
             reinterpret_cast<uint32_t*>(scp)[warp - 8] = b;
           }
         }
@@ -968,7 +982,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
         const uint4 all = *reinterpret_cast<const uint4*>(tops);
         const uint32_t ex = max(1u, max(max(all.x, all.y), max(all.z, all.w)) >> 23);
         const float down = __uint_as_float(ex == 254 ? 0x00400000u : (254 - ex) << 23);
-        if (i == 0) *reinterpret_cast<uint32_t*>(scp + 16) = ex << 23;
+        const uint4 vall = *reinterpret_cast<const uint4*>(tops + 4);
+        const int vx = min(250, max(8, int(max(max(vall.x, vall.y), max(vall.z, vall.w)) >> 23)));
+        if (j == ub || vx > vex + 3) vex = vx;
+        if (i == 0) *reinterpret_cast<uint2*>(scp + 16) = make_uint2(ex << 23, uint32_t(vex - kValueBits));
         mbar_arrive(&bars->sc[kv & 3]);
         uint32_t k_hi, k_lo, v_hi, v_lo;
         {
@@ -976,11 +993,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
           const __half hi = __float2half_rn(sc), lo = __float2half_rn(sc - __half2float(hi));
           k_hi = uint32_t(__half_as_ushort(hi)) * 0x10001u;
           k_lo = uint32_t(__half_as_ushort(lo)) * 0x10001u;
-          const float vz = v_fine ? vsc : 0.0f, vh = __bfloat162float(__float2bfloat16_rn(vz));
-          v_hi = f32_to_bf16x2(vh, vh);
-          v_lo = f32_to_bf16x2(vz - vh, vz - vh);
+          const float vz = v_fine ? vsc * __uint_as_float(uint32_t(254 + kValueBits - vex) << 23) : 0.0f;
+          const __half vh = __float2half_rn(vz), vl = __float2half_rn(vz - __half2float(vh));
+          v_hi = uint32_t(__half_as_ushort(vh)) * 0x10001u;
+          v_lo = uint32_t(__half_as_ushort(vl)) * 0x10001u;
         }
-        auto store = [&](uint8_t* tile, const uint4 (&x)[CH], bool value, uint32_t s_hi, uint32_t s_lo) {
+        auto store = [&](uint8_t* tile, const uint4 (&x)[CH], uint32_t s_hi, uint32_t s_lo) {
           uint8_t* row = tile + i * 128;
           const int turn = i & 7;
 #pragma unroll
@@ -991,26 +1009,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
             for (int e = 0; e < OUT; ++e) {
               uint32_t o[4];
               if constexpr (BITS == 4) {
-                if (value) bf_of4(wd[e], o);
-                else half_of4(wd[e], o);
+                half_of4(wd[e], o);
               } else {
-                if (value) {
-                  bf_of8(wd[2 * e], o[0], o[1]);
-                  bf_of8(wd[2 * e + 1], o[2], o[3]);
-                } else {
-                  half_of8(wd[2 * e], o[0], o[1]);
-                  half_of8(wd[2 * e + 1], o[2], o[3]);
-                }
+                half_of8(wd[2 * e], o[0], o[1]);
+                half_of8(wd[2 * e + 1], o[2], o[3]);
               }
 #pragma unroll
-              for (int y = 0; y < 4; ++y)
-                o[y] = value ? bfma2(o[y], s_hi, bfma2(o[y], s_lo, 0x80008000u)) : hfma2(o[y], s_hi, hfma2(o[y], s_lo, 0x80008000u));
+              for (int y = 0; y < 4; ++y) o[y] = hfma2(o[y], s_hi, hfma2(o[y], s_lo, 0x80008000u));
               const int c = OUT * k + e;  // chunk of the position's row
               *reinterpret_cast<uint4*>(row + (c / 8) * 16384 + ((c % 8) ^ turn) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
             }
           }
         };
-        store(smem + F::K + st * F::TILE, kr, false, k_hi, k_lo);
+        store(smem + F::K + st * F::TILE, kr, k_hi, k_lo);
         fence_proxy_async_smem();
         mbar_arrive(&bars->kfull[st]);
         // the next unit's codes are on their way while this one's are waited for and unpacked
@@ -1020,7 +1031,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
         ok = round == 0 || mbar_wait(&bars->vempty[st], (round - 1) & 1u);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        store(smem + F::V + st * F::TILE, vr, true, v_hi, v_lo);
+        store(smem + F::V + st * F::TILE, vr, v_hi, v_lo);
         fence_proxy_async_smem();
         mbar_arrive(&bars->vfull[st]);
         load(a.v_codes, vec, vr);
@@ -1031,7 +1042,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
     regs_less<80>();
     if (warp == 12) {
       // ---------------- products: the warp waits, one thread issues ----------------
-      constexpr uint32_t id_s = instr_desc(false, 128, false), id_o = instr_desc(true, D, true);
+      constexpr uint32_t id_s = instr_desc(128, false), id_o = instr_desc(D, true);
       const uint32_t base = smem_u32(smem);
       // descriptors of the tiles: the upper word is the same for all, the lower one holds the address
       const uint64_t dk = desc_sw128(base, 16, 1024), dv = desc_sw128(base + F::V, 16384, 1024);
