@@ -176,3 +176,19 @@ def test_binding_refuses_tensors_that_do_not_fit():
 def test_cache_shapes():
     assert hit.kv_cache_shapes(10, 16, 8, 128, 4) == ((10, 8, 16, 64), (10, 8, 16))
     assert hit.kv_cache_shapes(10, 16, 8, 128, 8) == ((10, 8, 16, 128), (10, 8, 16))
+
+
+def test_workspace_sizes_and_refusals(lib):
+    """Small calls need the parts of two tiles for each block; prompts the queries and larger tiles too."""
+    size = lib.rht_kv_workspace_bytes
+    assert 0 < size(4, 8, 2, 128, 1) == size(1 << 20, 8, 2, 128, 1)
+    assert size(4096, 8, 2, 128, 4096) >= 4096 * 8 * (128 * 2 + 4)
+    assert size(4096, 8, 2, 256, 4096) == size(1, 8, 2, 256, 1)
+    assert size(10, 8, 2, 64, 1 << 40) == size(10, 8, 2, 64, 10)  # no more new tokens than tokens
+    for bad in ((0, 8, 2, 128, 1), (4, 7, 2, 128, 1), (4, 8, 0, 128, 1), (4, 8, 2, 96, 1), (4, 8, 2, 128, 0)):
+        assert size(*bad) == 0
+    for tokens, max_new in ((4, 1), (4096, 4096)):
+        need = size(tokens, 8, 2, 128, max_new)
+        for kw in ({"ws": None}, {"nws": need - 1}, {"nws": 0}):
+            assert attend(lib, kv(), tokens=tokens, max_new=max_new, **kw) == _lib.HIT_EWORKSPACE
+        assert attend(lib, kv(), tokens=tokens, max_new=max_new, ws=FAKE + 4, nws=need) == _lib.HIT_EALIGN
