@@ -29,14 +29,15 @@ int cuda_status(cudaError_t e, const char* what) {
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 constexpr int64_t kMaxTokens = int64_t(1) << 31;
-constexpr int64_t kFewRows = 64;
+constexpr int64_t kFewRows = 64, kFewRows256 = 64;
 
 // Sequences with up to kFewRows query rows for a key/value head go to the kernel
 // that streams the codes once for 16 rows (an SM takes 7 cycles for a position and
 // 16 rows), the others to the one that works on 256 rows at a time (40 cycles for a
 // position, whatever the rows).  Each launch leaves the other's sequences alone, so that
 // max_new decides only whether the second kind is needed.
-bool few_only(int64_t max_new, int64_t group, int head_dim) { return head_dim == 256 || max_new * group <= kFewRows; }
+int64_t few_rows(int head_dim) { return head_dim == 256 ? kFewRows256 : kFewRows; }
+bool few_only(int64_t max_new, int64_t group, int head_dim) { return max_new * group <= few_rows(head_dim); }
 
 // Checks what the three calls share and fills `a`.  `rope`: whether the call
 // uses the rotary fields.
@@ -219,8 +220,8 @@ int rht_kv_attention(const hit_kv* kv, const void* q, void* out, int64_t tokens,
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (few_only(t.max_new, t.group, a.head_dim)) return cuda_status(hit::launch_kv_few(a, t, st), fn);
   hit::KvAttn few = t;
-  few.rows_hi = few.max_new = kFewRows;
-  t.rows_lo = kFewRows + 1;
+  few.rows_hi = few.max_new = few_rows(a.head_dim);
+  t.rows_lo = few.rows_hi + 1;
   r = cuda_status(hit::launch_kv_prompt_queries(a, t, st), fn);
   if (r == HIT_OK) r = cuda_status(hit::launch_kv_few(a, few, st), fn);
   return r ? r : cuda_status(hit::launch_kv_prompt(a, t, st), fn);

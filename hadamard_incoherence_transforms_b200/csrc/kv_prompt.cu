@@ -30,7 +30,6 @@ __device__ unsigned int g_wait_timeouts_kv = 0;
 
 namespace {
 
-constexpr int kRows = 256;      // query rows of a unit
 constexpr int kKeys = 128;      // positions of a unit
 constexpr int kThreads = 16 * 32;  // warps 14 and 15 are idle: registers are dealt out to groups of four warps
 constexpr int kCtas = 148;
@@ -40,9 +39,17 @@ constexpr int kValueBits = 4;      // the largest scale of a segment's first uni
 
 template <int D>
 struct Prompt {
-  static constexpr int BLK = D / 64;             // 64-element column blocks of an operand
-  static constexpr int TILE = BLK * 128 * 128;   // 128 vectors of D 16-bit elements
-  static constexpr int Q = 0, K = 2 * TILE, V = 4 * TILE, SC = 6 * TILE;
+  // Heads of 256 have room for one half of 128 rows (256 columns of O, 64 KB tiles),
+  // and for one stage of keys and of values.
+  static constexpr int HALVES = D == 256 ? 1 : 2;
+  static constexpr int ROWS = 128 * HALVES;      // query rows of a unit
+  static constexpr uint32_t STAGES = HALVES;
+  static constexpr int TILE = D * 2 * 128;       // 128 vectors of D 16-bit elements
+  static constexpr int Q = 0, K = HALVES * TILE, V = K + STAGES * TILE, SC = V + STAGES * TILE;
+  // registers of a thread of the four groups of warps; the launch has 4 x 128
+  static constexpr int SOFTMAX = D == 256 ? 192 : 160, UNPACK = D == 256 ? 208 : 112, OTHER = 80, IDLE = 24;
+  static_assert(SOFTMAX + (HALVES == 2 ? SOFTMAX : IDLE) + UNPACK + OTHER <= 512, "registers");
+  static constexpr float NORM = D == 64 ? 0.125f : D == 256 ? 0.0625f : 0.08838834764831845f;
   // ring of four units: which positions exist (128 bits), the powers of two of the scales
   static constexpr int SC_STAGE = 32;
   static constexpr int TS = SC + 4 * SC_STAGE;   // the largest scales of each unpacking warp, two units
@@ -72,9 +79,10 @@ static_assert(sizeof(Bars) <= 512, "barrier block");
 // with 3; one prompt of 1,024 tokens 93 and 82; 2 and 5 lie within 2 %.
 constexpr int kLead = 3;
 // Units of row tile rt of a sequence: [first, first + count).
+template <int ROWS>
 __device__ __forceinline__ void tile_units(const KvAttn& t, const KvSeq& q, int rt, int& first, int& count) {
   const int64_t rows = int64_t(q.n) * t.group;
-  const int64_t r0 = int64_t(rt) * kRows, r1 = min(rows, r0 + kRows);
+  const int64_t r0 = int64_t(rt) * ROWS, r1 = min(rows, r0 + ROWS);
   const int64_t i0 = r0 / t.group, i1 = (r1 - 1) / t.group;
   const int64_t hi = t.causal ? max(int64_t(0), min(q.hi, q.pos0 + i1 + 1)) : q.hi;
   const int64_t lo = t.window > 0 ? min(hi, max(int64_t(0), q.pos0 + i0 - t.window + 1)) : 0;
@@ -83,11 +91,12 @@ __device__ __forceinline__ void tile_units(const KvAttn& t, const KvSeq& q, int 
 }
 
 // Units of a sequence for one key/value head, found by a warp.
+template <int ROWS>
 __device__ __forceinline__ int64_t head_units_warp(const KvAttn& t, const KvSeq& q, int lane) {
   int64_t sum = 0;
   for (int rt = lane; rt < q.row_tiles; rt += 32) {
     int f, c;
-    tile_units(t, q, rt, f, c);
+    tile_units<ROWS>(t, q, rt, f, c);
     sum += c + kLead;
   }
 #pragma unroll
@@ -96,32 +105,34 @@ __device__ __forceinline__ int64_t head_units_warp(const KvAttn& t, const KvSeq&
 }
 
 // Units of sequences s0 .. s0 + 31, one to a lane.
+template <int ROWS>
 __device__ __forceinline__ int64_t chunk_units(const KvArgs& a, const KvAttn& t, int s0, int lane) {
   int64_t w = 0;
   bool big = false;
   if (s0 + lane < a.seqs) {
-    const KvSeq q = kv_seq<kRows, kKeys, 0>(a, t, s0 + lane);
+    const KvSeq q = kv_seq<ROWS, kKeys, 0>(a, t, s0 + lane);
     if (kv_mine(t, q)) {
       big = q.row_tiles > 4;
       for (int rt = 0; rt < q.row_tiles && !big; ++rt) {
         int f, c;
-        tile_units(t, q, rt, f, c);
+        tile_units<ROWS>(t, q, rt, f, c);
         w += c + kLead;
       }
     }
   }
   for (uint32_t m = __ballot_sync(0xffffffffu, big); m; m &= m - 1) {
     const int k = __ffs(m) - 1;
-    const int64_t v = head_units_warp(t, kv_seq<kRows, kKeys, 0>(a, t, s0 + k), lane);
+    const int64_t v = head_units_warp<ROWS>(t, kv_seq<ROWS, kKeys, 0>(a, t, s0 + k), lane);
     if (lane == k) w = v;
   }
   return w * a.hk;
 }
 
 // One warp finds the CTA's share and where it begins.
+template <int ROWS>
 __device__ __forceinline__ void plan_warp(const KvArgs& a, const KvAttn& t, Bars* b, int lane) {
   int64_t total = 0;
-  for (int s0 = 0; s0 < a.seqs; s0 += 32) total += chunk_units(a, t, s0, lane);
+  for (int s0 = 0; s0 < a.seqs; s0 += 32) total += chunk_units<ROWS>(a, t, s0, lane);
 #pragma unroll
   for (int i = 16; i; i >>= 1) total += __shfl_xor_sync(0xffffffffu, total, i);
   const int64_t ctas = max(int64_t(1), min(int64_t(gridDim.x), (total + 1) / 2));
@@ -131,7 +142,7 @@ __device__ __forceinline__ void plan_warp(const KvArgs& a, const KvAttn& t, Bars
   int64_t base = 0;
   if (u0 < u1) {
     for (int s0 = 0; s0 < a.seqs; s0 += 32) {
-      const int64_t v = chunk_units(a, t, s0, lane);
+      const int64_t v = chunk_units<ROWS>(a, t, s0, lane);
       int64_t x = v;
 #pragma unroll
       for (int i = 1; i < 32; i <<= 1) {
@@ -150,14 +161,14 @@ __device__ __forceinline__ void plan_warp(const KvArgs& a, const KvAttn& t, Bars
   }
   int h = 0, rt = 0, x0 = 0;
   if (seq < a.seqs) {
-    const KvSeq q = kv_seq<kRows, kKeys, 0>(a, t, seq);
-    const int64_t per = head_units_warp(t, q, lane);
+    const KvSeq q = kv_seq<ROWS, kKeys, 0>(a, t, seq);
+    const int64_t per = head_units_warp<ROWS>(t, q, lane);
     h = int((u0 - base) / per);
     int64_t r = u0 - base - h * per;
     for (int r0 = 0; r0 < q.row_tiles; r0 += 32) {
       int f, v = 0;
       if (r0 + lane < q.row_tiles) {
-        tile_units(t, q, r0 + lane, f, v);
+        tile_units<ROWS>(t, q, r0 + lane, f, v);
         v += kLead;
       }
       int64_t x = v;
@@ -212,12 +223,13 @@ struct SegmentRing {
 
 // The walk over the share: segments into the ring, then one that ends it.
 // True unless a wait ran out.
+template <int ROWS>
 __device__ __forceinline__ bool walk(const KvArgs& a, const KvAttn& t, const Bars* b, SegmentRing* ring,
                                      volatile int* abort) {
   int s = b->seq, h = b->h, rt = b->rt, x0 = b->x0;
   int64_t left = b->units, at = int64_t(blockIdx.x) * b->total / b->ctas;
   KvSeq q{};
-  if (left > 0) q = kv_seq<kRows, kKeys, 0>(a, t, s);
+  if (left > 0) q = kv_seq<ROWS, kKeys, 0>(a, t, s);
   // the next row tile
   auto step = [&]() {
     x0 = 0;
@@ -226,7 +238,7 @@ __device__ __forceinline__ bool walk(const KvArgs& a, const KvAttn& t, const Bar
       if (++h == a.hk) {
         h = 0;
         do {
-          q = kv_seq<kRows, kKeys, 0>(a, t, ++s);
+          q = kv_seq<ROWS, kKeys, 0>(a, t, ++s);
         } while (q.n == 0 || !kv_mine(t, q));
       }
     }
@@ -234,7 +246,7 @@ __device__ __forceinline__ bool walk(const KvArgs& a, const KvAttn& t, const Bar
   for (int n = 0;; ++n) {
     int first = 0, count = 0, x1 = 0;
     while (left > 0) {
-      tile_units(t, q, rt, first, count);
+      tile_units<ROWS>(t, q, rt, first, count);
       x1 = int(min(int64_t(count + kLead), x0 + left));
       if (x1 > kLead) break;
       // no unit of keys: what is left begins in the next CTA
@@ -252,8 +264,8 @@ __device__ __forceinline__ bool walk(const KvArgs& a, const KvAttn& t, const Bar
       g.hi = q.hi;
       g.s = s;
       g.h = h;
-      g.row0 = rt * kRows;
-      g.nr = int(min(int64_t(kRows), int64_t(q.n) * t.group - g.row0));
+      g.row0 = rt * ROWS;
+      g.nr = int(min(int64_t(ROWS), int64_t(q.n) * t.group - g.row0));
       int ub = INT32_MAX, ue = 0;
       for (int k = 0; k < 2; ++k) {
         Half f{min(128, max(0, g.nr - 128 * k)), 0, 0, 0, 0, 0};
@@ -586,7 +598,7 @@ struct QueryWork {
 };
 template <int D>
 __host__ __device__ __forceinline__ QueryWork<D> query_work_of(void* ws, int64_t tokens, int heads) {
-  uint8_t* p = static_cast<uint8_t*>(ws) + kv_work_bytes<D, kRows>(kCtas);
+  uint8_t* p = static_cast<uint8_t*>(ws) + kv_work_bytes<D, Prompt<D>::ROWS>(kCtas);
   QueryWork<D> w;
   w.rows = reinterpret_cast<__half*>(p);
   w.factors = reinterpret_cast<float*>(p + size_t(tokens) * heads * D * 2);
@@ -612,7 +624,7 @@ __global__ void __launch_bounds__(256) k_kv_query(const KvArgs a, const KvAttn t
     }
   }
   kv_turns(a, turns, threadIdx.x, blockDim.x);
-  kv_factors<D, 0>(factors, a.k_signs, (D == 64 ? 0.125f : 0.08838834764831845f) * 1.4426950408889634f * t.scale);
+  kv_factors<D, 0>(factors, a.k_signs, Prompt<D>::NORM * 1.4426950408889634f * t.scale);
   __syncthreads();
   for (int i = threadIdx.x; i < nt * a.n_freq; i += blockDim.x) {
     const int j = i / a.n_freq, f = i - j * a.n_freq;
@@ -690,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
     for (int i = 0; i < 4; ++i) mbar_init(&bars->sc[i], 128);
     for (int i = 0; i < kSegments; ++i) {
       mbar_init(&ring.full[i], 1);
-      mbar_init(&ring.empty[i], 13);  // 8 softmax, 4 unpacking, 1 issuing warps
+      mbar_init(&ring.empty[i], 4 * F::HALVES + 5);  // softmax, 4 unpacking, 1 issuing warps
     }
     mbar_init(&bars->done, 1);
     bars->abort = 0;
@@ -707,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
     const uint32_t b = __ballot_sync(0xffffffffu, a.v_signs != nullptr && __ldg(a.v_signs + 32 * (warp - 4) + lane) < 0);
     if (lane == 0) v_neg[warp - 4] = b;
   }
-  if (warp == 0) plan_warp(a, t, bars, lane);
+  if (warp == 0) plan_warp<F::ROWS>(a, t, bars, lane);
   fence_before();
   __syncthreads();
   fence_after();
@@ -719,8 +731,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
 
   Follow w{&ring};
   int more = 1;
-  if (warp < 8) {
-    regs_more<160>();
+  if (warp < 4 * F::HALVES) {
+    regs_more<F::SOFTMAX>();
     // the launch begins before the one ahead of it has ended: the queries, and
     // the workspace that is written here, are its
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -729,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
     const uint32_t lane_at = tmem + (uint32_t(32 * (warp & 3)) << 16);
     const uint32_t s_at = lane_at + F::S_COL + 128 * hf, o_at = lane_at + F::O_COL + D * hf;
     const QueryWork<D> queries = query_work_of<D>(t.ws, a.tokens, t.heads);
-    const KvWork work = kv_work_of<D, kRows>(t.ws, gridDim.x);
+    const KvWork work = kv_work_of<D, Prompt<D>::ROWS>(t.ws, gridDim.x);
     uint32_t ns = 0, no = 0;  // score units and outputs seen so far
     uint32_t kv0 = 0;         // units converted before this segment
     KvPart open;
@@ -822,12 +834,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
       }
       // ---------------- the half's result ----------------
       const bool any = f.js < f.je;
-      const size_t slot_row = (2 * size_t(blockIdx.x) + (g.begins ? 1 : 0)) * kRows + 128 * hf + r;
+      const size_t slot_row = (2 * size_t(blockIdx.x) + (g.begins ? 1 : 0)) * Prompt<D>::ROWS + 128 * hf + r;
       const float up = __uint_as_float(ve << 23);
-      const float inv = l == 0.0f ? 0.0f : (D == 64 ? 0.125f : 0.08838834764831845f) / l * up;
+      const float inv = l == 0.0f ? 0.0f : F::NORM / l * up;
       if (f.rows > 0) {  // by the whole warp: tensor memory is read together
         if (g.whole) {
-          constexpr int N = D / 64;  // the transform's last stage joins the halves of 128 elements
+          constexpr int N = D / 64;  // the transform's last stages join the runs of 64 elements
 #pragma unroll 1
           for (int b = 0; b < N; ++b) {
             float x[64];
@@ -837,14 +849,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
 #pragma unroll
               for (int i = 0; i < 32; ++i) x[32 * c + i] = 0.0f;
               if (any) {
-                tmem_load32_now(o_at + 32 * c, u);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) x[32 * c + 8 * (i / 8) + v_elem<BITS>(i % 8)] = __uint_as_float(u[i]) * inv;
-                if constexpr (N == 2) {
-                  tmem_load32_now(o_at + 64 + 32 * c, u);
+                for (int e = 0; e < N; ++e) {
+                  const float f = __popc(b & e) & 1 ? -inv : inv;
+                  tmem_load32_now(o_at + 64 * e + 32 * c, u);
 #pragma unroll
-                  for (int i = 0; i < 32; ++i)
-                    x[32 * c + 8 * (i / 8) + v_elem<BITS>(i % 8)] += __uint_as_float(u[i]) * (b == 0 ? inv : -inv);
+                  for (int i = 0; i < 32; ++i) {
+                    float& y = x[32 * c + 8 * (i / 8) + v_elem<BITS>(i % 8)];
+                    y = fmaf(__uint_as_float(u[i]), f, y);
+                  }
                 }
               }
             }
@@ -901,9 +914,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
     }
     if (more < 0 && lane == 0) give_up();
     if (threadIdx.x == 0) work.part[2 * blockIdx.x + 1] = open;
+  } else if (warp < 8) {
+    regs_less<F::IDLE>();
   } else if (warp < 12) {
     // ---------------- codes to operands, a thread a position ----------------
-    regs_less<112>();
+    if constexpr (F::UNPACK < 128) regs_less<F::UNPACK>();
+    else regs_more<F::UNPACK>();
     const int i = threadIdx.x - 256;
     uint32_t kv = 0;
     bool ok = true;
@@ -949,8 +965,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
         load(a.v_codes, vec, vr);
       }
       for (int j = ub; j < ue; ++j, ++kv) {
-        const int st = kv & 1;
-        const uint32_t round = kv >> 1;
+        const uint32_t st = kv % F::STAGES, round = kv / F::STAGES;
         const int page = page_of(j + 1);
         ok = !*abort && (round == 0 || mbar_wait(&bars->kempty[st], (round - 1) & 1u));
         ok = __all_sync(0xffffffffu, ok);
@@ -1039,7 +1054,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
     }
     if ((!ok || more < 0) && !*abort) give_up();
   } else {
-    regs_less<80>();
+    regs_less<F::OTHER>();
     if (warp == 12) {
       // ---------------- products: the warp waits, one thread issues ----------------
       constexpr uint32_t id_s = instr_desc(128, false), id_o = instr_desc(D, true);
@@ -1059,9 +1074,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
           const uint32_t kn = kv + 1;
           bool have_v = false, have_k = false;
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
+          for (int hf = 0; hf < F::HALVES; ++hf) {
             if (ok && j >= js[hf] && j < je[hf]) {
-              if (!have_v) ok = mbar_wait(&bars->vfull[kv & 1], (kv >> 1) & 1u);
+              if (!have_v) ok = mbar_wait(&bars->vfull[kv % F::STAGES], (kv / F::STAGES) & 1u);
               have_v = true;
               ok = ok && !*abort && mbar_wait(&bars->p[hf], np[hf] & 1u);
               ok = __all_sync(0xffffffffu, ok);
@@ -1069,23 +1084,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
               ++np[hf];
               fence_after();
               if (elect_one()) {
-                const uint32_t lo = v_lo + (kv & 1) * (F::TILE >> 4);
+                const uint32_t lo = v_lo + (kv % F::STAGES) * (F::TILE >> 4);
                 const bool add = j > js[hf];
 #pragma unroll
                 for (int k = 0; k < kKeys / 16; ++k)
                   mma_ts(tmem + F::O_COL + D * hf, tmem + F::S_COL + 128 * hf + 8 * k, lo + k * 128, v_hi, id_o, k > 0 || add);
                 commit(&bars->o[hf]);
+                if (F::HALVES == 1) commit(&bars->vempty[0]);  // ahead of the next scores: it is the only stage
               }
             }
             if (ok && j + 1 >= js[hf] && j + 1 < je[hf]) {
-              if (!have_k) ok = mbar_wait(&bars->kfull[kn & 1], (kn >> 1) & 1u);
+              if (!have_k) ok = mbar_wait(&bars->kfull[kn % F::STAGES], (kn / F::STAGES) & 1u);
               have_k = true;
               if (ok && j + 1 == js[hf]) ok = mbar_wait(&bars->q[hf], nq[hf]++ & 1u);
               ok = __all_sync(0xffffffffu, ok && !*abort);
               if (!ok) break;
               fence_after();
               if (elect_one()) {
-                const uint32_t lo_q = q_lo + hf * (F::TILE >> 4), lo_k = k_lo + (kn & 1) * (F::TILE >> 4);
+                const uint32_t lo_q = q_lo + hf * (F::TILE >> 4), lo_k = k_lo + (kn % F::STAGES) * (F::TILE >> 4);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
                   mma_ss(tmem + F::S_COL + 128 * hf, lo_q + (k / 4) * 1024 + 2 * (k % 4), lo_k + (k / 4) * 1024 + 2 * (k % 4),
@@ -1097,8 +1113,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
           }
           if (!ok) break;
           if (elect_one()) {
-            if (j >= ub) commit(&bars->vempty[kv & 1]);
-            if (j + 1 < ue) commit(&bars->kempty[kn & 1]);
+            if (F::HALVES == 2 && j >= ub) commit(&bars->vempty[kv % F::STAGES]);
+            if (j + 1 < ue) commit(&bars->kempty[kn % F::STAGES]);
           }
           __syncwarp();
         }
@@ -1109,7 +1125,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
       if (elect_one()) commit(&bars->done);
       if (!mbar_wait(&bars->done, 0u)) atomicAdd(&g_wait_timeouts_kv, 1u);
     } else if (warp == 13 && lane == 0) {
-      if (!walk(a, t, bars, &ring, abort)) give_up();
+      if (!walk<F::ROWS>(a, t, bars, &ring, abort)) give_up();
     }
   }
   __syncwarp();
@@ -1157,24 +1173,29 @@ cudaError_t go(const KvArgs& a, const KvAttn& t, cudaStream_t st) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kernel, a, t, make_fastdiv(uint32_t(t.group)));
   if (e != cudaSuccess) return e;
-  return launch_kv_join<D, kRows, 8>(a, t, kCtas, st);
+  return launch_kv_join<D, Prompt<D>::ROWS, 8>(a, t, kCtas, st);
 }
 
 }  // namespace
 
 size_t kv_prompt_bytes(int64_t tokens, int heads, int head_dim) {
   const size_t queries = size_t(tokens) * heads * (size_t(head_dim) * 2 + 4);
-  return (head_dim == 64 ? kv_work_bytes<64, kRows>(kCtas) : kv_work_bytes<128, kRows>(kCtas)) + queries;
+  const size_t parts = head_dim == 64    ? kv_work_bytes<64, Prompt<64>::ROWS>(kCtas)
+                       : head_dim == 128 ? kv_work_bytes<128, Prompt<128>::ROWS>(kCtas)
+                                         : kv_work_bytes<256, Prompt<256>::ROWS>(kCtas);
+  return parts + queries;
 }
 
 // Two launches; nothing else may write the workspace's part for queries between them.
 cudaError_t launch_kv_prompt_queries(const KvArgs& a, const KvAttn& t, cudaStream_t st) {
   if (a.head_dim == 64) return a.bits == 4 ? prepare<64, 4>(a, t, st) : prepare<64, 8>(a, t, st);
-  return a.bits == 4 ? prepare<128, 4>(a, t, st) : prepare<128, 8>(a, t, st);
+  if (a.head_dim == 128) return a.bits == 4 ? prepare<128, 4>(a, t, st) : prepare<128, 8>(a, t, st);
+  return a.bits == 4 ? prepare<256, 4>(a, t, st) : prepare<256, 8>(a, t, st);
 }
 cudaError_t launch_kv_prompt(const KvArgs& a, const KvAttn& t, cudaStream_t st) {
   if (a.head_dim == 64) return a.bits == 4 ? go<64, 4>(a, t, st) : go<64, 8>(a, t, st);
-  return a.bits == 4 ? go<128, 4>(a, t, st) : go<128, 8>(a, t, st);
+  if (a.head_dim == 128) return a.bits == 4 ? go<128, 4>(a, t, st) : go<128, 8>(a, t, st);
+  return a.bits == 4 ? go<256, 4>(a, t, st) : go<256, 8>(a, t, st);
 }
 
 cudaError_t wait_timeouts_kv(unsigned long long* count, bool reset) {

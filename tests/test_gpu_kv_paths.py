@@ -53,6 +53,9 @@ def test_many_sequences(seqs, most, g, d):
     ([513, 40, 1, 300], [513, 1000, 700, 301], 4, 0, True, 128, 4),
     ([129, 700], [2000, 700], 1, 129, True, 128, 8),
     ([260, 65], [1500, 400], 3, 0, False, 64, 8),
+    ([300, 40, 1, 129], [1400, 900, 300, 129], 2, 0, True, 256, 8),
+    ([257, 500], [700, 500], 1, 200, True, 256, 4),
+    ([90], [2000], 5, 0, False, 256, 8),
     ([70, 66, 68, 90, 64, 65, 1], [70, 500, 131, 90, 64, 257, 900], 1, 0, True, 128, 4),
 ])
 def test_prompts_over_several_blocks(new, lens, g, window, causal, d, bits):
@@ -86,12 +89,12 @@ def test_scores_that_grow_along_the_cache(new, g, up):
     check_attention(got, want, size, torch.float32)
 
 
-@pytest.mark.parametrize("new,g", [(1, 4), (40, 4)])
+@pytest.mark.parametrize("new,g,d", [(1, 4, 64), (40, 4, 64), (80, 4, 256)])
 @pytest.mark.parametrize("kind", ["up", "down", "mixed", "first"])
-def test_values_of_very_different_size(new, g, kind):
+def test_values_of_very_different_size(new, g, d, kind):
     """Value scales that grow or fall by 2^4 every 100 positions, ones that differ by 2^16 from neighbour to
     neighbour, and a first position of next to nothing that takes nearly all of the weight."""
-    n, d = 900, 64
+    n = 900
     c = Cache(43, [n], 1, d, 8, 16).fill()
     for p in range(n):
         page, i = kc.slot(c.table, c.pages, c.page, 0, p)

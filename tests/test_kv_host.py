@@ -183,7 +183,7 @@ def test_workspace_sizes_and_refusals(lib):
     size = lib.rht_kv_workspace_bytes
     assert 0 < size(4, 8, 2, 128, 1) == size(1 << 20, 8, 2, 128, 1)
     assert size(4096, 8, 2, 128, 4096) >= 4096 * 8 * (128 * 2 + 4)
-    assert size(4096, 8, 2, 256, 4096) == size(1, 8, 2, 256, 1)
+    assert size(4096, 8, 2, 256, 4096) >= 4096 * 8 * (256 * 2 + 4)
     assert size(10, 8, 2, 64, 1 << 40) == size(10, 8, 2, 64, 10)  # no more new tokens than tokens
     for bad in ((0, 8, 2, 128, 1), (4, 7, 2, 128, 1), (4, 8, 0, 128, 1), (4, 8, 2, 96, 1), (4, 8, 2, 128, 0)):
         assert size(*bad) == 0
