@@ -405,7 +405,7 @@ HIT_API int harp_blocks(const float* theta, const int8_t* theta_q, float theta_s
  *   [tokens, heads, head_dim], strided as k.  Arithmetic: queries (behind a
  *   power of two of their own row) fp16, scores and outputs summed in fp32,
  *   softmax in fp32.  Where a sequence has at most 64 query rows (tokens *
- *   heads / kv_heads) for a key/value head, or head_dim is 256, codes and
+ *   heads / kv_heads; 32 with head_dim 256) for a key/value head, codes and
  *   scales enter exactly and probabilities (times the value's scale) are
  *   rounded to bf16; in longer chunks keys, values and probabilities are
  *   rounded to fp16, keys relative to the largest scale of their 128 positions
