@@ -28,6 +28,8 @@ int cuda_status(cudaError_t e, const char* what) {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+constexpr int64_t kMaxTokens = int64_t(1) << 31;
+
 // Sequences with up to kFewRows query rows for a key/value head go to the kernel
 // that streams the codes once for 16 rows (an SM takes 7 cycles for a position and
 // 16 rows), the others to the one that works on 256 rows at a time (40 cycles for a
