@@ -31,6 +31,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 namespace hit {
 
@@ -55,8 +56,8 @@ struct Prompt {
   static constexpr int TILE = D * 2 * 128;       // 128 vectors of D 16-bit elements
   static constexpr int Q = 0, K = HALVES * TILE, V = K + STAGES * TILE, SC = V + STAGES * TILE;
   // registers of a thread of the four groups of warps; the launch has 4 x 128
-  static constexpr int SOFTMAX = D == 256 ? 192 : 160, UNPACK = D == 256 ? 208 : 112, OTHER = 80, IDLE = 24;
-  static_assert(SOFTMAX + (HALVES == 2 ? SOFTMAX : IDLE) + UNPACK + OTHER <= 512, "registers");
+  static constexpr int SOFTMAX = D == 256 ? 208 : 160, UNPACK = 112, OTHER = 80;
+  static_assert(SOFTMAX + (HALVES == 2 ? SOFTMAX : UNPACK) + UNPACK + OTHER <= 512, "registers");
   static constexpr float NORM = D == 64 ? 0.125f : D == 256 ? 0.0625f : 0.08838834764831845f;
   // ring of four units: which positions exist (128 bits), the powers of two of the scales
   static constexpr int SC_STAGE = 32;
@@ -707,10 +708,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
       mbar_init(&bars->p[i], 128);
       mbar_init(&bars->o[i], 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&bars->sc[i], 128);
+    for (int i = 0; i < 4; ++i) mbar_init(&bars->sc[i], F::HALVES == 2 ? 128 : 256);
     for (int i = 0; i < kSegments; ++i) {
       mbar_init(&ring.full[i], 1);
-      mbar_init(&ring.empty[i], 4 * F::HALVES + 5);  // softmax, 4 unpacking, 1 issuing warps
+      mbar_init(&ring.empty[i], 13);  // softmax and unpacking warps, and the issuing one
     }
     mbar_init(&bars->done, 1);
     bars->abort = 0;
@@ -922,145 +923,162 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
     }
     if (more < 0 && lane == 0) give_up();
     if (threadIdx.x == 0) work.part[2 * blockIdx.x + 1] = open;
-  } else if (warp < 8) {
-    regs_less<F::IDLE>();
   } else if (warp < 12) {
     // ---------------- codes to operands, a thread a position ----------------
-    if constexpr (F::UNPACK < 128) regs_less<F::UNPACK>();
-    else regs_more<F::UNPACK>();
-    const int i = threadIdx.x - 256;
-    uint32_t kv = 0;
-    bool ok = true;
-    while (ok && (more = w.next(lane)) > 0) {
-      const int ub = w.seg().ub, ue = w.seg().ue, h = w.seg().h;
-      const int64_t hi = w.seg().hi;
-      const int32_t* const pages = a.table + int64_t(w.seg().s) * a.ld_table;
-      uint4 kr[CH], vr[CH];
-      float ksc = 0.0f, vsc = 0.0f;
-      int vex = 0;  // exponent of the largest value scale that the segment's values are relative to
-      bool in = false;
-      // the page of this thread's position in unit j (-1: there is none), and its vector in that page
-      auto page_of = [&](int j) {
-        const int64_t p = int64_t(j) * kKeys + i;
-        int page = -1;
-        if (j < ue && p < hi) load4(page, pages + (p >> a.log_page));
-        return page;
-      };
-      auto vector_of = [&](int j, int page) {
-        const int64_t p = int64_t(j) * kKeys + i;
-        in = page >= 0 && page < a.pages;
-        return (((int64_t(page) * a.hk + h) << a.log_page) + (p & ((int64_t(1) << a.log_page) - 1)));
-      };
-      auto load = [&](const uint8_t* codes, int64_t vec, uint4 (&x)[CH]) {
-#pragma unroll
-        for (int k = 0; k < CH; ++k) {
-          x[k] = make_uint4(0, 0, 0, 0);
-          if (in) load16(x[k], codes + vec * VB + 16 * k);
-        }
-      };
-      auto load_scales = [&](int64_t vec) {
-        ksc = vsc = 0.0f;
-        if (in) {
-          load4(ksc, a.k_scales + vec);
-          load4(vsc, a.v_scales + vec);
-        }
-      };
-      int64_t vec = 0;
-      if (ub < ue) {
-        vec = vector_of(ub, page_of(ub));
-        load_scales(vec);
-        load(a.k_codes, vec, kr);
-        load(a.v_codes, vec, vr);
-      }
-      for (int j = ub; j < ue; ++j, ++kv) {
-        const uint32_t st = kv % F::STAGES, round = kv / F::STAGES;
-        const int page = page_of(j + 1);
-        ok = !*abort && (round == 0 || mbar_wait(&bars->kempty[st], (round - 1) & 1u));
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        // The scales are folded into the operands, with one rounding: a product
-        // with a scale in two parts, hi and the rest.  Keys are relative to a
-        // power of two of the unit's largest scale, so that fp16 holds them, values
-        // to one of the largest scale of the segment's first unit: a later unit
-        // whose scales are more than 2^3 times as large takes its own, and O is
-        // brought to it.  Codes times scales then stay below 2^15, and scales down to
-        // 2^-18 of the largest keep 11 bits (bf16 values cost the result 2^-8 of
-        // each, 0.0029 in place of 0.0017 in all).  A position whose scale is not
-        // finite becomes NaN in its scores, and only there.
-        uint32_t* const tops = reinterpret_cast<uint32_t*>(smem + F::TS + (kv & 1) * 32);
-        uint8_t* const scp = smem + F::SC + (kv & 3) * F::SC_STAGE;
-        const bool k_fine = (__float_as_uint(ksc) & 0x7f800000u) != 0x7f800000u;
-        const bool v_fine = (__float_as_uint(vsc) & 0x7f800000u) != 0x7f800000u;
-        {
-          const uint32_t top = __reduce_max_sync(0xffffffffu, k_fine ? __float_as_uint(ksc) & 0x7fffffffu : 0u);
-          const uint32_t vtop = __reduce_max_sync(0xffffffffu, v_fine ? __float_as_uint(vsc) & 0x7fffffffu : 0u);
-          const uint32_t b = __ballot_sync(0xffffffffu, in);
-          if (lane == 0) {
-            tops[warp - 8] = top;
-            tops[warp - 4] = vtop;
-            reinterpret_cast<uint32_t*>(scp)[warp - 8] = b;
-          }
-        }
-        asm volatile("bar.sync 3, 128;" ::: "memory");
-        const uint4 all = *reinterpret_cast<const uint4*>(tops);
-        const uint32_t ex = max(1u, max(max(all.x, all.y), max(all.z, all.w)) >> 23);
-        const float down = __uint_as_float(ex == 254 ? 0x00400000u : (254 - ex) << 23);
-        const uint4 vall = *reinterpret_cast<const uint4*>(tops + 4);
-        const int vx = min(250, max(8, int(max(max(vall.x, vall.y), max(vall.z, vall.w)) >> 23)));
-        if (j == ub || vx > vex + 3) vex = vx;
-        if (i == 0) *reinterpret_cast<uint2*>(scp + 16) = make_uint2(ex << 23, uint32_t(vex - kValueBits));
-        mbar_arrive(&bars->sc[kv & 3]);
-        uint32_t k_hi, k_lo, v_hi, v_lo;
-        {
-          const float sc = v_fine ? ksc * down : __uint_as_float(0x7fc00000u);
-          const __half hi = __float2half_rn(sc), lo = __float2half_rn(sc - __half2float(hi));
-          k_hi = uint32_t(__half_as_ushort(hi)) * 0x10001u;
-          k_lo = uint32_t(__half_as_ushort(lo)) * 0x10001u;
-          const float vz = v_fine ? vsc * __uint_as_float(uint32_t(254 + kValueBits - vex) << 23) : 0.0f;
-          const __half vh = __float2half_rn(vz), vl = __float2half_rn(vz - __half2float(vh));
-          v_hi = uint32_t(__half_as_ushort(vh)) * 0x10001u;
-          v_lo = uint32_t(__half_as_ushort(vl)) * 0x10001u;
-        }
-        auto store = [&](uint8_t* tile, const uint4 (&x)[CH], uint32_t s_hi, uint32_t s_lo) {
-          uint8_t* row = tile + i * 128;
-          const int turn = i & 7;
+    regs_less<F::UNPACK>();
+    const int i = threadIdx.x & 127;
+    // keys and values by the same threads, or (heads of 256) the values by warps 4-7:
+    // 1,024 tokens on 12,000 (32 heads on 8) take 706 us with 8 bits and 660 with 4; with
+    // one group 1,010 and 674
+    auto unpack = [&](auto keys_too, auto values_too) {
+      constexpr bool KEYS = decltype(keys_too)::value, VALUES = decltype(values_too)::value;
+      uint32_t kv = 0;
+      bool ok = true;
+      while (ok && (more = w.next(lane)) > 0) {
+        const int ub = w.seg().ub, ue = w.seg().ue, h = w.seg().h;
+        const int64_t hi = w.seg().hi;
+        const int32_t* const pages = a.table + int64_t(w.seg().s) * a.ld_table;
+        uint4 kr[CH], vr[CH];
+        float ksc = 0.0f, vsc = 0.0f;
+        int vex = 0;  // exponent of the largest value scale that the segment's values are relative to
+        bool in = false;
+        // the page of this thread's position in unit j (-1: there is none), and its vector in that page
+        auto page_of = [&](int j) {
+          const int64_t p = int64_t(j) * kKeys + i;
+          int page = -1;
+          if (j < ue && p < hi) load4(page, pages + (p >> a.log_page));
+          return page;
+        };
+        auto vector_of = [&](int j, int page) {
+          const int64_t p = int64_t(j) * kKeys + i;
+          in = page >= 0 && page < a.pages;
+          return (((int64_t(page) * a.hk + h) << a.log_page) + (p & ((int64_t(1) << a.log_page) - 1)));
+        };
+        auto load = [&](const uint8_t* codes, int64_t vec, uint4 (&x)[CH]) {
 #pragma unroll
           for (int k = 0; k < CH; ++k) {
-            const uint32_t wd[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-            constexpr int OUT = 128 / (8 * BITS);  // 16-byte chunks of operand from 16 bytes of codes
-#pragma unroll
-            for (int e = 0; e < OUT; ++e) {
-              uint32_t o[4];
-              if constexpr (BITS == 4) {
-                half_of4(wd[e], o);
-              } else {
-                half_of8(wd[2 * e], o[0], o[1]);
-                half_of8(wd[2 * e + 1], o[2], o[3]);
-              }
-#pragma unroll
-              for (int y = 0; y < 4; ++y) o[y] = hfma2(o[y], s_hi, hfma2(o[y], s_lo, 0x80008000u));
-              const int c = OUT * k + e;  // chunk of the position's row
-              *reinterpret_cast<uint4*>(row + (c / 8) * 16384 + ((c % 8) ^ turn) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
-            }
+            x[k] = make_uint4(0, 0, 0, 0);
+            if (in) load16(x[k], codes + vec * VB + 16 * k);
           }
         };
-        store(smem + F::K + st * F::TILE, kr, k_hi, k_lo);
-        fence_proxy_async_smem();
-        mbar_arrive(&bars->kfull[st]);
-        // the next unit's codes are on their way while this one's are waited for and unpacked
-        vec = vector_of(j + 1, page);
-        load_scales(vec);
-        load(a.k_codes, vec, kr);
-        ok = round == 0 || mbar_wait(&bars->vempty[st], (round - 1) & 1u);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        store(smem + F::V + st * F::TILE, vr, v_hi, v_lo);
-        fence_proxy_async_smem();
-        mbar_arrive(&bars->vfull[st]);
-        load(a.v_codes, vec, vr);
+        auto load_scales = [&](int64_t vec) {
+          ksc = vsc = 0.0f;
+          if (in) {
+            if constexpr (KEYS) load4(ksc, a.k_scales + vec);
+            load4(vsc, a.v_scales + vec);
+          }
+        };
+        int64_t vec = 0;
+        if (ub < ue) {
+          vec = vector_of(ub, page_of(ub));
+          load_scales(vec);
+          if constexpr (KEYS) load(a.k_codes, vec, kr);
+          if constexpr (VALUES) load(a.v_codes, vec, vr);
+        }
+        for (int j = ub; j < ue; ++j, ++kv) {
+          const uint32_t st = kv % F::STAGES, round = kv / F::STAGES;
+          const int page = page_of(j + 1);
+          ok = !*abort && (round == 0 || mbar_wait(KEYS ? &bars->kempty[st] : &bars->vempty[st], (round - 1) & 1u));
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          // The scales are folded into the operands, with one rounding: a product
+          // with a scale in two parts, hi and the rest.  Keys are relative to a
+          // power of two of the unit's largest scale, so that fp16 holds them, values
+          // to one of the largest scale of the segment's first unit: a later unit
+          // whose scales are more than 2^3 times as large takes its own, and O is
+          // brought to it.  Codes times scales then stay below 2^15, and scales down to
+          // 2^-18 of the largest keep 11 bits (bf16 values cost the result 2^-8 of
+          // each, 0.0029 in place of 0.0017 in all).  A position whose scale is not
+          // finite becomes NaN in its scores, and only there.
+          uint32_t* const tops = reinterpret_cast<uint32_t*>(smem + F::TS + (kv & 1) * 32);
+          uint8_t* const scp = smem + F::SC + (kv & 3) * F::SC_STAGE;
+          const bool k_fine = (__float_as_uint(ksc) & 0x7f800000u) != 0x7f800000u;
+          const bool v_fine = (__float_as_uint(vsc) & 0x7f800000u) != 0x7f800000u;
+          {
+            const uint32_t top = KEYS ? __reduce_max_sync(0xffffffffu, k_fine ? __float_as_uint(ksc) & 0x7fffffffu : 0u) : 0u;
+            const uint32_t vtop = VALUES ? __reduce_max_sync(0xffffffffu, v_fine ? __float_as_uint(vsc) & 0x7fffffffu : 0u) : 0u;
+            const uint32_t b = __ballot_sync(0xffffffffu, in);
+            if (lane == 0) {
+              if (KEYS) tops[warp & 3] = top, reinterpret_cast<uint32_t*>(scp)[warp & 3] = b;
+              if (VALUES) tops[4 + (warp & 3)] = vtop;
+            }
+          }
+          asm volatile("bar.sync %0, 128;" ::"n"(KEYS ? 3 : 4) : "memory");
+          float down = 0.0f;
+          if constexpr (KEYS) {
+            const uint4 all = *reinterpret_cast<const uint4*>(tops);
+            const uint32_t ex = max(1u, max(max(all.x, all.y), max(all.z, all.w)) >> 23);
+            down = __uint_as_float(ex == 254 ? 0x00400000u : (254 - ex) << 23);
+            if (i == 0) *reinterpret_cast<uint32_t*>(scp + 16) = ex << 23;
+          }
+          if constexpr (VALUES) {
+            const uint4 all = *reinterpret_cast<const uint4*>(tops + 4);
+            const int vx = min(250, max(8, int(max(max(all.x, all.y), max(all.z, all.w)) >> 23)));
+            if (j == ub || vx > vex + 3) vex = vx;
+            if (i == 0) *reinterpret_cast<uint32_t*>(scp + 20) = uint32_t(vex - kValueBits);
+          }
+          mbar_arrive(&bars->sc[kv & 3]);
+          uint32_t k_hi, k_lo, v_hi, v_lo;
+          {
+            const float sc = v_fine ? ksc * down : __uint_as_float(0x7fc00000u);
+            const __half hi = __float2half_rn(sc), lo = __float2half_rn(sc - __half2float(hi));
+            k_hi = uint32_t(__half_as_ushort(hi)) * 0x10001u;
+            k_lo = uint32_t(__half_as_ushort(lo)) * 0x10001u;
+            const float vz = v_fine ? vsc * __uint_as_float(uint32_t(254 + kValueBits - vex) << 23) : 0.0f;
+            const __half vh = __float2half_rn(vz), vl = __float2half_rn(vz - __half2float(vh));
+            v_hi = uint32_t(__half_as_ushort(vh)) * 0x10001u;
+            v_lo = uint32_t(__half_as_ushort(vl)) * 0x10001u;
+          }
+          auto store = [&](uint8_t* tile, const uint4 (&x)[CH], uint32_t s_hi, uint32_t s_lo) {
+            uint8_t* row = tile + i * 128;
+            const int turn = i & 7;
+#pragma unroll
+            for (int k = 0; k < CH; ++k) {
+              const uint32_t wd[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+              constexpr int OUT = 128 / (8 * BITS);  // 16-byte chunks of operand from 16 bytes of codes
+#pragma unroll
+              for (int e = 0; e < OUT; ++e) {
+                uint32_t o[4];
+                if constexpr (BITS == 4) {
+                  half_of4(wd[e], o);
+                } else {
+                  half_of8(wd[2 * e], o[0], o[1]);
+                  half_of8(wd[2 * e + 1], o[2], o[3]);
+                }
+#pragma unroll
+                for (int y = 0; y < 4; ++y) o[y] = hfma2(o[y], s_hi, hfma2(o[y], s_lo, 0x80008000u));
+                const int c = OUT * k + e;  // chunk of the position's row
+                *reinterpret_cast<uint4*>(row + (c / 8) * 16384 + ((c % 8) ^ turn) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+              }
+            }
+          };
+          if constexpr (KEYS) {
+            store(smem + F::K + st * F::TILE, kr, k_hi, k_lo);
+            fence_proxy_async_smem();
+            mbar_arrive(&bars->kfull[st]);
+          }
+          // the next unit's codes are on their way while this one's are waited for and unpacked
+          vec = vector_of(j + 1, page);
+          load_scales(vec);
+          if constexpr (KEYS) load(a.k_codes, vec, kr);
+          if constexpr (VALUES) {
+            if constexpr (KEYS) {
+              ok = round == 0 || mbar_wait(&bars->vempty[st], (round - 1) & 1u);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+            }
+            store(smem + F::V + st * F::TILE, vr, v_hi, v_lo);
+            fence_proxy_async_smem();
+            mbar_arrive(&bars->vfull[st]);
+            load(a.v_codes, vec, vr);
+          }
+        }
       }
-    }
-    if ((!ok || more < 0) && !*abort) give_up();
+      if ((!ok || more < 0) && !*abort) give_up();
+    };
+    if constexpr (F::HALVES == 2) unpack(std::true_type{}, std::true_type{});
+    else if (warp < 8) unpack(std::false_type{}, std::true_type{});
+    else unpack(std::true_type{}, std::false_type{});
   } else {
     regs_less<F::OTHER>();
     if (warp == 12) {
