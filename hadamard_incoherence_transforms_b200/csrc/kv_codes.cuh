@@ -1,6 +1,4 @@
-// Stored codes to matrix operands, in registers and without an error: fp16, or
-// bf16 for values whose other operand is a probability times a scale, which spans
-// more than fp16's range.
+// Stored codes to fp16 matrix operands, in registers and without an error.
 #pragma once
 #include <stdint.h>
 
@@ -21,16 +19,6 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
   return r;
 }
-__device__ __forceinline__ uint32_t badd2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t bfma2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t r;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  return r;
-}
 
 // Eight 4-bit codes -> (0, 4), (1, 5), (2, 6), (3, 7) as fp16 pairs: 0x6400 | u
 // is 1024 + u, and 1024 + 16 u for the upper nibble of a byte.
@@ -46,18 +34,14 @@ __device__ __forceinline__ void half_of8(uint32_t w, uint32_t& a, uint32_t& b) {
   a = hadd2(__byte_perm(w, 0x64646464u, 0x4140), 0xe480e480u);  // 1024 + u - 1152
   b = hadd2(__byte_perm(w, 0x64646464u, 0x4342), 0xe480e480u);
 }
-// x: two runs of 16 bits of codes.  4-bit codes -> (code n of the low run, code n
-// of the high one), n = 0 .. 3, as bf16 pairs.
-__device__ __forceinline__ void bf_of4(uint32_t x, uint32_t (&b)[4]) {
+// x: two runs of 16 bits of codes -> (code n of the low run, code n of the high one).
+__device__ __forceinline__ void half_runs4(uint32_t x, uint32_t (&b)[4]) {
 #pragma unroll
-  for (int n = 0; n < 4; ++n) b[n] = badd2(and_or(x >> (4 * n), 0x000f000fu, 0x43004300u), 0xc308c308u);  // 128 + u - 136
+  for (int n = 0; n < 4; ++n) b[n] = hadd2(and_or(x >> (4 * n), 0x000f000fu, 0x64006400u), 0xe408e408u);  // 1024 + u - 1032
 }
-// 8-bit codes, n = 0, 1: 16 h + l - 128 from its nibbles, every step exact.
-__device__ __forceinline__ void bf_of8(uint32_t x, uint32_t& b0, uint32_t& b1) {
-  const uint32_t l0 = and_or(x, 0x000f000fu, 0x43004300u), h0 = and_or(x >> 4, 0x000f000fu, 0x43004300u);
-  const uint32_t l1 = and_or(x >> 8, 0x000f000fu, 0x43004300u), h1 = and_or(x >> 12, 0x000f000fu, 0x43004300u);
-  b0 = badd2(bfma2(h0, 0x41804180u, 0xc510c510u), l0);  // (128 + h) * 16 - 2304 + 128 + l
-  b1 = badd2(bfma2(h1, 0x41804180u, 0xc510c510u), l1);
+__device__ __forceinline__ void half_runs8(uint32_t x, uint32_t& b0, uint32_t& b1) {
+  b0 = hadd2(and_or(x, 0x00ff00ffu, 0x64006400u), 0xe480e480u);  // 1024 + u - 1152
+  b1 = hadd2(and_or(x >> 8, 0x00ff00ffu, 0x64006400u), 0xe480e480u);
 }
 
 // d += A B for 16 x 8 x 16, fp16 operands.

@@ -12,15 +12,15 @@
 //   K to fp16: a code under the exponent of 1024 (one logic operation), minus
 //     the offset -- exact; the query is scaled to [-2, 2) by a power of two of
 //     its own row, so that fp16 holds it to 2^-11 whatever its size;
-//   V to bf16, as the other operand (probability times the value's scale)
-//     spans more than fp16's range.
+//   V to fp16 likewise; the other operand, probability times the value's scale, is
+//     rounded to fp16, the scale relative to a power of two that each warp keeps.
 // O^T += V^T P^T takes P^T from the score accumulators with one 8x8 transpose
 // per 8 positions.  Scales never touch the codes: the key's multiplies its
 // score, the value's its probability.
 //
 // 64 sequences of 300 to 8,000 positions (32 heads on 8, head 128, 4 bits) take
-// 78 us, two of 125,000 (8 bits) 74 us: 3.3 and 3.7 TB/s, where the loop over the
-// units alone runs at 5.6 to 5.9 TB/s.  The rest is finding the share, preparing
+// 84 us, two of 125,000 (8 bits) 70 us: 3.0 and 3.9 TB/s, where the loop over the
+// units alone runs at 5.3 to 5.9 TB/s.  The rest is finding the share, preparing
 // the queries and the first loads (about 10 us), uneven ends, and the joining
 // launch (8 us).
 #include "kv_codes.cuh"
@@ -37,7 +37,8 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStages = 3;
-constexpr float kGrow = 65536.0f;
+constexpr float kGrow = 2048.0f;  // a lane's share of a column's sum above which it gets a new reference
+constexpr float kRoom = 4.0f;     // a reference's own probability is 2^kRoom
 constexpr int kLead = 16;  // beginning a pair takes a CTA about as long as 16 units
 
 // Positions of a unit: stages of 2 to 4 KB (8 KB for heads of 256); three of
@@ -53,14 +54,6 @@ struct Few {
   static constexpr int KS = D / 16;
 };
 
-__device__ __forceinline__ void mma_b16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
-      "%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -360,6 +353,7 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
       m[n][1] = 8 * n + 2 * c4 + 1 < nr ? -INFINITY : 0.0f;
       l[n][0] = l[n][1] = 0.0f;
     }
+    int ve = -200;  // exponent of the power of two that o is relative to; none yet
     int stage = 0;
     for (int i = 0; i < nu; ++i) {
       issue();
@@ -437,8 +431,8 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
       }
 
       // Probabilities against the columns' references so far.  A reference is a
-      // maximum of scores seen before and is only raised where a lane's share of a
-      // column adds up to more than kGrow (bf16 and fp32 hold 2^16 as well as 1).
+      // maximum of scores seen before, less kRoom, and is only raised where a lane's
+      // share of a column adds up to more than kGrow.
       float pr[MT][NT][4], add[NT][2];
       auto powers = [&]() {
 #pragma unroll
@@ -473,6 +467,7 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
 #pragma unroll
             for (int b = 4; b < 32; b <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, b));
             // a column's lanes agree on v, and so on its new reference
+            v -= kRoom;
             f[k] = v > m[n][k] ? ex2(m[n][k] - v) : 1.0f;
             m[n][k] = fmaxf(m[n][k], v);
             l[n][k] *= f[k];
@@ -484,13 +479,31 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
         }
         powers();
       }
+      // Values' scales relative to a power of two: that of the largest one so far, or
+      // up to 2^3 below it.  Probability times scale is then below 2^15, and fp16 keeps 11
+      // bits of it down to 2^-18 of the largest (bf16 kept 8: an error of 0.0024 of the
+      // result in place of 0.0017; 80 us in place of 84 with 4 bits, 75 of 70 with 8).
+      uint32_t big = __float_as_uint(vs[lane & (TK - 1)]) & 0x7fffffffu;
+      if (big >= 0x7f800000u || !(full || ((there >> (lane & (TK - 1))) & 1))) big = 0;
+      const int ex = min(250, max(8, int(__reduce_max_sync(0xffffffffu, big) >> 23)));
+      if (ex > ve + 3) {
+        const float f = __uint_as_float(uint32_t(max(0, 127 + ve - ex)) << 23);
+#pragma unroll
+        for (int d = 0; d < OM; ++d)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[d][n][e] *= f;
+        ve = ex;
+      }
+      const float vdown = __uint_as_float(uint32_t(254 - ve) << 23);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         l[n][0] += add[n][0];
         l[n][1] += add[n][1];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          const float v0 = vs[16 * mt + r8], v1 = vs[16 * mt + r8 + 8];
+          const float v0 = vs[16 * mt + r8] * vdown, v1 = vs[16 * mt + r8 + 8] * vdown;
 #pragma unroll
           for (int e = 0; e < 4; ++e) pr[mt][n][e] *= e < 2 ? v0 : v1;
         }
@@ -508,8 +521,9 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
         uint32_t pb[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          pb[n][0] = transpose8x8(f32_to_bf16x2(pr[mt][n][0], pr[mt][n][1]));
-          pb[n][1] = transpose8x8(f32_to_bf16x2(pr[mt][n][2], pr[mt][n][3]));
+          const __half2 lo2 = __floats2half2_rn(pr[mt][n][0], pr[mt][n][1]), hi2 = __floats2half2_rn(pr[mt][n][2], pr[mt][n][3]);
+          pb[n][0] = transpose8x8(*reinterpret_cast<const uint32_t*>(&lo2));
+          pb[n][1] = transpose8x8(*reinterpret_cast<const uint32_t*>(&hi2));
         }
         // 16-bit units of codes, of two neighbouring positions a register: matrix
         // lane / 8 of a load is positions 8 (lane / 8 % 2) ... of piece x or x + 1
@@ -522,19 +536,19 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
           for (int y = 0; y < 2; ++y) {  // positions 0-7 and 8-15 of piece x + y
             if constexpr (BITS == 4) {
               uint32_t ab[4], cd[4];
-              bf_of4(v[2 * y], ab);
-              bf_of4(v[2 * y + 1], cd);
+              half_runs4(v[2 * y], ab);
+              half_runs4(v[2 * y + 1], cd);
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
-                mma_b16(o[2 * (x + y)][n], ab[0], ab[1], cd[0], cd[1], pb[n][0], pb[n][1]);
-                mma_b16(o[2 * (x + y) + 1][n], ab[2], ab[3], cd[2], cd[3], pb[n][0], pb[n][1]);
+                mma_f16(o[2 * (x + y)][n], ab[0], ab[1], cd[0], cd[1], pb[n][0], pb[n][1]);
+                mma_f16(o[2 * (x + y) + 1][n], ab[2], ab[3], cd[2], cd[3], pb[n][0], pb[n][1]);
               }
             } else {
               uint32_t a0, a1, c0, c1;
-              bf_of8(v[2 * y], a0, a1);
-              bf_of8(v[2 * y + 1], c0, c1);
+              half_runs8(v[2 * y], a0, a1);
+              half_runs8(v[2 * y + 1], c0, c1);
 #pragma unroll
-              for (int n = 0; n < NT; ++n) mma_b16(o[x + y][n], a0, a1, c0, c1, pb[n][0], pb[n][1]);
+              for (int n = 0; n < NT; ++n) mma_f16(o[x + y][n], a0, a1, c0, c1, pb[n][0], pb[n][1]);
             }
           }
         }
@@ -545,6 +559,7 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
     __syncthreads();
 
     // join the warps; shared memory is free now
+    const float up = __uint_as_float(uint32_t(max(0, ve)) << 23);
     float* mo = reinterpret_cast<float*>(smem);                       // [kWarps][ROWS][D]
     float2* ms = reinterpret_cast<float2*>(mo + kWarps * ROWS * D);   // [kWarps][ROWS]
     static_assert(kWarps * ROWS * (D * 4 + 8) <= kStages * kWarps * F::STAGE, "join buffer");
@@ -561,11 +576,11 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
 #pragma unroll
           for (int x = 0; x < CH; ++x)
             *reinterpret_cast<float4*>(dst + 32 * x + 4 * r8) =
-                make_float4(o[2 * x][n][k], o[2 * x][n][k + 2], o[2 * x + 1][n][k], o[2 * x + 1][n][k + 2]);
+                make_float4(o[2 * x][n][k] * up, o[2 * x][n][k + 2] * up, o[2 * x + 1][n][k] * up, o[2 * x + 1][n][k + 2] * up);
         } else {  // tile x: elements 16 x + 2 r8, + 1
 #pragma unroll
           for (int x = 0; x < CH; ++x)
-            *reinterpret_cast<float2*>(dst + 16 * x + 2 * r8) = make_float2(o[x][n][k], o[x][n][k + 2]);
+            *reinterpret_cast<float2*>(dst + 16 * x + 2 * r8) = make_float2(o[x][n][k] * up, o[x][n][k + 2] * up);
         }
       }
     }

@@ -404,14 +404,14 @@ HIT_API int harp_blocks(const float* theta, const int8_t* theta_q, float theta_s
  *   only) only j > p - window.  A token that sees nothing gets 0.  q, out:
  *   [tokens, heads, head_dim], strided as k.  Arithmetic: queries (behind a
  *   power of two of their own row) fp16, scores and outputs summed in fp32,
- *   softmax in fp32.  Where a sequence has at most 64 query rows (tokens *
- *   heads / kv_heads; 32 with head_dim 256) for a key/value head, codes and
- *   scales enter exactly and probabilities (times the value's scale) are
- *   rounded to bf16; in longer chunks keys, values and probabilities are
- *   rounded to fp16, keys relative to the largest scale of their 128 positions
- *   and values to the largest one of the positions before theirs and of those
- *   128: 11 bits of a key down to 2^-14 of that scale, of a value to 2^-18, and
- *   fewer below.  Two calls on the same inputs give the same bits.
+ *   softmax in fp32; probabilities and the values' scales enter the products in
+ *   fp16, values relative to the largest scale of the positions before theirs
+ *   and of their block of up to 128: 11 bits of what is not below 2^-18 of it.
+ *   Where a sequence has at most 64 query rows (tokens * heads / kv_heads; 32
+ *   with head_dim 256) for a key/value head, codes and the keys' scales enter
+ *   exactly; in longer chunks keys are rounded to fp16 too, relative to the
+ *   largest scale of their 128 positions (11 bits down to 2^-14 of it).  Two calls
+ *   on the same inputs give the same bits.
  *   max_new: an upper bound of n_s (any value >= 1 gives right results; a tight
  *   one saves launches and workspace).  Needs rht_kv_workspace_bytes(tokens,
  *   heads, kv_heads, head_dim, max_new) bytes of 16-byte aligned workspace,
