@@ -484,7 +484,11 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
       // bits of it down to 2^-18 of the largest (bf16 kept 8: an error of 0.0024 of the
       // result in place of 0.0017; 80 us in place of 84 with 4 bits, 75 of 70 with 8).
       uint32_t big = __float_as_uint(vs[lane & (TK - 1)]) & 0x7fffffffu;
-      if (big >= 0x7f800000u || !(full || ((there >> (lane & (TK - 1))) & 1))) big = 0;
+      if (!full) {  // of positions that a row of the tile sees: others hold anything
+        const int64_t p = p0 + (lane & (TK - 1));
+        if (!((there >> (lane & (TK - 1))) & 1) || p < lo_min || p >= hi_max) big = 0;
+      }
+      if (big >= 0x7f800000u) big = 0;
       const int ex = min(250, max(8, int(__reduce_max_sync(0xffffffffu, big) >> 23)));
       if (ex > ve + 3) {
         const float f = __uint_as_float(uint32_t(max(0, 127 + ve - ex)) << 23);

@@ -107,6 +107,18 @@ def test_values_of_very_different_size(new, g, d, kind):
     check_attention(got, want, size, torch.float32, kind)
 
 
+@pytest.mark.parametrize("new,g", [([1, 2], 2), ([1, 1], 16), ([70, 40], 2)])
+@pytest.mark.parametrize("page", [4, 64])
+@pytest.mark.parametrize("left", [1e30, 3e38, np.inf, np.nan])
+def test_slots_that_hold_no_position(new, g, page, left):
+    """What a page was left with behind a sequence's end says nothing about the values before it."""
+    c = Cache(45, [75, 130], 1, 64, 4, page).fill()
+    for scales in (c.k[1], c.v[1]):
+        scales[np.isnan(scales)] = left
+    got, want, size = attend_both(c, new, g, torch.float32)
+    check_attention(got, want, size, torch.float32)
+
+
 @pytest.mark.parametrize("new", [[2, 1], [50, 3]])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("d", [64, 128])
