@@ -226,3 +226,24 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for x in got:
         assert all(torch.equal(y, want[j % 2]) for j, y in enumerate(x))
+
+
+@pytest.mark.parametrize("d,g", [(64, 2), (128, 1), (256, 2)])
+@pytest.mark.parametrize("window", [0, 20])
+def test_prompts_with_missing_pages_and_tokens_before_the_start(d, g, window):
+    """Long chunks of which a part lies before position 0 (rows of 0), pages that are not there in the middle, a
+    sequence of which nothing exists, and tokens of no sequence around them."""
+    c = Cache(73, [300, 90, 150, 40], 1, d, 4, 16).fill()
+    c.table[0, 3:7] = c.pages + 5
+    c.table[0, 9] = -1
+    c.table[2, :] = -1
+    c.lens[1] = 30                       # 90 tokens, 60 of them before the sequence's start
+    cu = cu_of([140, 90, 130, 40], first=3)
+    n = int(cu[-1]) + 2
+    q, q64 = heads(c.r, n, g, d, torch.bfloat16)
+    want, size = kc.attention(q64, c.k, c.v, c.table, cu, c.lens, 4, c.k_signs, c.v_signs, d ** -0.5, True, window)
+    out = torch.full((n, g, d), 5.0, device="cuda", dtype=torch.bfloat16)
+    hit.rht_kv_attention(q, *c.on(), torch.from_numpy(cu).cuda(), **c.signs(), window=window, out=out)
+    assert (out[:3] == 5.0).all() and (out[-2:] == 5.0).all()
+    check_attention(out, want, size, torch.bfloat16)
+    assert (out[3 + 140:3 + 140 + 60] == 0).all() and (out[3 + 230:3 + 360] == 0).all()
