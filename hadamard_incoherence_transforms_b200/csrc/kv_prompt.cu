@@ -71,6 +71,7 @@ struct Prompt {
 struct Bars {
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sc[4];
   uint64_t q[2], s[2], p[2], o[2], done;
+  uint64_t met[2];  // the unpacking warps of keys and of values have each written their largest scales
   uint32_t tmem;
   int abort;
   // the CTA's share
@@ -707,6 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
       mbar_init(&bars->s[i], 1);
       mbar_init(&bars->p[i], 128);
       mbar_init(&bars->o[i], 1);
+      mbar_init(&bars->met[i], 4);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&bars->sc[i], F::HALVES == 2 ? 128 : 256);
     for (int i = 0; i < kSegments; ++i) {
@@ -1003,7 +1005,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
               if (VALUES) tops[4 + (warp & 3)] = vtop;
             }
           }
-          asm volatile("bar.sync %0, 128;" ::"n"(KEYS ? 3 : 4) : "memory");
+          // the group's four warps meet, with the limit of every wait: one of them may have given up
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->met[KEYS ? 0 : 1]);
+          ok = mbar_wait(&bars->met[KEYS ? 0 : 1], kv & 1u);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
           float down = 0.0f;
           if constexpr (KEYS) {
             const uint4 all = *reinterpret_cast<const uint4*>(tops);
