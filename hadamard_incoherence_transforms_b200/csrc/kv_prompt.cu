@@ -71,7 +71,6 @@ struct Prompt {
 struct Bars {
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sc[4];
   uint64_t q[2], s[2], p[2], o[2], done;
-  uint64_t met[2];  // the unpacking warps of keys and of values have each written their largest scales
   uint32_t tmem;
   int abort;
   // the CTA's share
@@ -708,7 +707,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
       mbar_init(&bars->s[i], 1);
       mbar_init(&bars->p[i], 128);
       mbar_init(&bars->o[i], 1);
-      mbar_init(&bars->met[i], 4);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&bars->sc[i], F::HALVES == 2 ? 128 : 256);
     for (int i = 0; i < kSegments; ++i) {
@@ -936,7 +934,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
       constexpr bool KEYS = decltype(keys_too)::value, VALUES = decltype(values_too)::value;
       uint32_t kv = 0;
       bool ok = true;
-      while (ok && (more = w.next(lane)) > 0) {
+      // The group's four warps meet once a unit.  The barrier has no limit of its own, so
+      // a warp one of whose waits (which have a limit) has run out comes to the next meeting
+      // all the same, says so there, and all of them leave.
+      auto meet = [&]() { asm volatile("bar.sync %0, 128;" ::"n"(KEYS ? 3 : 4) : "memory"); };
+      constexpr uint32_t kFailed = ~0u;  // in the place of a warp's largest scale
+      bool told = false;                 // one of them leaves
+      while (ok && !told && (more = w.next(lane)) > 0) {
         const int ub = w.seg().ub, ue = w.seg().ue, h = w.seg().h;
         const int64_t hi = w.seg().hi;
         const int32_t* const pages = a.table + int64_t(w.seg().s) * a.ld_table;
@@ -980,9 +984,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
         for (int j = ub; j < ue; ++j, ++kv) {
           const uint32_t st = kv % F::STAGES, round = kv / F::STAGES;
           const int page = page_of(j + 1);
-          ok = !*abort && (round == 0 || mbar_wait(KEYS ? &bars->kempty[st] : &bars->vempty[st], (round - 1) & 1u));
+          ok = ok && !*abort && (round == 0 || mbar_wait(KEYS ? &bars->kempty[st] : &bars->vempty[st], (round - 1) & 1u));
           ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
           // The scales are folded into the operands, with one rounding: a product
           // with a scale in two parts, hi and the rest.  Keys are relative to a
           // power of two of the unit's largest scale, so that fp16 holds them, values
@@ -1001,29 +1004,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
             const uint32_t vtop = VALUES ? __reduce_max_sync(0xffffffffu, v_fine ? __float_as_uint(vsc) & 0x7fffffffu : 0u) : 0u;
             const uint32_t b = __ballot_sync(0xffffffffu, in);
             if (lane == 0) {
-              if (KEYS) tops[warp & 3] = top, reinterpret_cast<uint32_t*>(scp)[warp & 3] = b;
-              if (VALUES) tops[4 + (warp & 3)] = vtop;
+              if (KEYS) tops[warp & 3] = ok ? top : kFailed, reinterpret_cast<uint32_t*>(scp)[warp & 3] = b;
+              if (VALUES) tops[4 + (warp & 3)] = ok ? vtop : kFailed;
             }
           }
-          // the group's four warps meet, with the limit of every wait: one of them may have given up
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars->met[KEYS ? 0 : 1]);
-          ok = mbar_wait(&bars->met[KEYS ? 0 : 1], kv & 1u);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
+          meet();
           float down = 0.0f;
           if constexpr (KEYS) {
             const uint4 all = *reinterpret_cast<const uint4*>(tops);
             const uint32_t ex = max(1u, max(max(all.x, all.y), max(all.z, all.w)) >> 23);
+            told = ex > 255;
             down = __uint_as_float(ex == 254 ? 0x00400000u : (254 - ex) << 23);
             if (i == 0) *reinterpret_cast<uint32_t*>(scp + 16) = ex << 23;
           }
           if constexpr (VALUES) {
             const uint4 all = *reinterpret_cast<const uint4*>(tops + 4);
-            const int vx = min(250, max(8, int(max(max(all.x, all.y), max(all.z, all.w)) >> 23)));
+            const uint32_t vtop = max(max(all.x, all.y), max(all.z, all.w)) >> 23;
+            told = vtop > 255;
+            const int vx = min(250, max(8, int(vtop)));
             if (j == ub || vx > vex + 3) vex = vx;
             if (i == 0) *reinterpret_cast<uint32_t*>(scp + 20) = uint32_t(vex - kValueBits);
           }
+          if (told) break;
           mbar_arrive(&bars->sc[kv & 3]);
           uint32_t k_hi, k_lo, v_hi, v_lo;
           {
@@ -1072,7 +1074,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
             if constexpr (KEYS) {
               ok = round == 0 || mbar_wait(&bars->vempty[st], (round - 1) & 1u);
               ok = __all_sync(0xffffffffu, ok);
-              if (!ok) break;
             }
             store(smem + F::V + st * F::TILE, vr, v_hi, v_lo);
             fence_proxy_async_smem();
@@ -1082,6 +1083,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
         }
       }
       if ((!ok || more < 0) && !*abort) give_up();
+      if (!told) {  // no unit is left for this warp: the others may be at the meeting of one
+        if (lane == 0 && (!ok || more < 0))
+          reinterpret_cast<uint32_t*>(smem + F::TS + (kv & 1) * 32)[(KEYS ? 0 : 4) + (warp & 3)] = kFailed;
+        meet();
+      }
     };
     if constexpr (F::HALVES == 2) unpack(std::true_type{}, std::true_type{});
     else if (warp < 8) unpack(std::false_type{}, std::true_type{});
