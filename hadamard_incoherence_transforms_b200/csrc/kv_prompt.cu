@@ -44,7 +44,8 @@ constexpr int kThreads = 16 * 32;  // warps 14 and 15 are idle: registers are de
 constexpr int kCtas = 148;
 constexpr float kGrow = 32768.0f;  // sum of 32 probabilities above which a row gets a new reference
 constexpr float kRoom = 4.0f;      // a reference's own probability is 2^kRoom
-constexpr int kValueBits = 4;      // the largest scale of a segment's first unit becomes 2^kValueBits or more
+constexpr int kValueBits = 4;      // the largest scale of the unit that a power of two was taken from becomes 2^kValueBits or more
+constexpr int kSpread = 8;         // scales down to 2^-kSpread of the largest share its power of two
 
 template <int D>
 struct Prompt {
@@ -59,11 +60,16 @@ struct Prompt {
   static constexpr int SOFTMAX = D == 256 ? 208 : 160, UNPACK = 112, OTHER = 80;
   static_assert(SOFTMAX + (HALVES == 2 ? SOFTMAX : UNPACK) + UNPACK + OTHER <= 512, "registers");
   static constexpr float NORM = D == 64 ? 0.125f : D == 256 ? 0.0625f : 0.08838834764831845f;
-  // ring of four units: which positions exist (128 bits), the powers of two of the scales
+  // ring of four units: which positions exist (128 bits), the powers of two of keys and of
+  // values, and whether any position of each unpacking warp has its own (4 + 4 bytes)
   static constexpr int SC_STAGE = 32;
   static constexpr int TS = SC + 4 * SC_STAGE;   // the largest scales of each unpacking warp, two units
-  static constexpr int BARS = TS + 64;
-  static constexpr int BYTES = BARS + 512 + 1024;
+  // ring of four units: the exponents of the keys' and of the values' own powers of two, a
+  // byte a position.  (Shared memory of more than 196 KB leaves a third of the L1 cache, and
+  // registers live there: 1.31 ms in place of 1.23 with 4 KB more.)
+  static constexpr int OWN = TS + 64, OWN_STAGE = 2 * kKeys;
+  static constexpr int BARS = OWN + 4 * OWN_STAGE;
+  static constexpr int BYTES = BARS + 240 + 1008;  // the last for the alignment of the tiles
   static constexpr int S_COL = 0, O_COL = 2 * 128;  // tensor memory columns
   static constexpr int COLS = 512;
 };
@@ -77,7 +83,7 @@ struct Bars {
   int64_t total, units;
   int ctas, seq, h, rt, x0;
 };
-static_assert(sizeof(Bars) <= 512, "barrier block");
+static_assert(sizeof(Bars) <= 240, "barrier block");
 
 // ---------------------------------------------------------------------------
 // The list of units.
@@ -402,6 +408,11 @@ __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&r)[16
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+__device__ __forceinline__ void tmem_store8(uint32_t at, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -448,6 +459,113 @@ struct UnitSoftmax {
   uint4 there;          // positions that exist
   int c_lo, c_hi;       // columns [c_lo, c_hi) are this row's
   float qu;             // the row's and the unit's power of two
+
+  // The same for a unit some of whose scales lie so far below the largest that their
+  // keys or values are held by powers of two of their own (own: their exponents, keys' ahead
+  // of values'; 0 where it is the unit's).  Scores are multiplied by the keys',
+  // and probabilities (not their sum) by the values', relative to a power of two
+  // 2^(ve - 127) that the row takes for O so that its largest product is 2^kRoom or more:
+  // what a row does not see, or gives no weight to, costs it no digits.  Two
+  // passes, as the largest product is wanted first; a function of its own, so that the
+  // usual case keeps its registers.
+  struct Row {
+    float m, l, fix;
+    uint32_t ve;
+  };
+  static __device__ __noinline__ Row run_apart(const UnitSoftmax u, const uint8_t* own, float qe, uint4 unit, float m, float l,
+                                               uint32_t ve) {
+    // unit: as in shared memory; only the runs of 32 positions that it names have bytes
+    auto score = [&](uint32_t v, int j) {
+      const uint32_t k = (unit.z >> (j / 32 * 8)) & 255 ? own[j] : 0;
+      return __uint_as_float(v) * __uint_as_float(k == 0 ? unit.x : k << 23) * qe;
+    };
+    auto exponent = [&](int j) {
+      const uint32_t v = (unit.w >> (j / 32 * 8)) & 255 ? own[kKeys + j] : 0;
+      return float(int(v == 0 ? unit.y : v) - 127);
+    };
+    float top = -INFINITY, heavy = -INFINITY, fix = 1.0f;
+#pragma unroll 1
+    for (int c = 0; c < 8; ++c) {
+      const uint32_t see = u.seen(c >> 1) >> (16 * (c & 1));
+      if (!__any_sync(0xffffffffu, (see & 0xffffu) != 0)) continue;
+      uint32_t v[16];
+      tmem_load16_now(u.s_at + 16 * c, v);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (!((see >> i) & 1)) continue;
+        const float x = score(v[i], 16 * c + i);
+        top = fmaxf(top, x);
+        heavy = fmaxf(heavy, x + exponent(16 * c + i));
+      }
+    }
+    if (m == -INFINITY ? top > m : top - m > 11.0f) {  // probabilities stay below 2^11
+      fix = ex2(m - (top - kRoom));                    // 0 for a first reference
+      m = top - kRoom;
+      l *= fix;
+    }
+    const float base = m == -INFINITY ? 0.0f : -m;
+    float shift = 0.0f;  // what the values' exponents are relative to
+    if (heavy > -INFINITY) {
+      shift = fminf(fmaxf(floorf(heavy + base) - kRoom, -126.0f), 127.0f);
+      ve = uint32_t(127 + int(shift));
+    }
+    // 16 columns at a time: their probabilities go where scores have been read before
+#pragma unroll 1
+    for (int c = 0; c < 8; ++c) {
+      const uint32_t see = u.seen(c >> 1) >> (16 * (c & 1));
+      uint32_t v[16], p[8];
+      tmem_load16_now(u.s_at + 16 * c, v);
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        float y[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int j = 16 * c + i + k;
+          const float x = (see >> (i + k)) & 1 ? score(v[i + k], j) + base : -INFINITY;
+          l += ex2(x);
+          y[k] = ex2(x + (exponent(j) - shift));
+        }
+        const __half2 h = __floats2half2_rn(y[0], y[1]);
+        p[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      tmem_store8(u.p_at + 8 * c, p);
+    }
+    return Row{m, l, fix, ve};
+  }
+
+  // O (times f) is to be brought to a power of two 2^d times as fine, the row's new ve.  Where
+  // it would leave fp32's range ve is raised, and the unit's probabilities, which are
+  // nothing beside it then, are lowered.  The factor for O, in Row::fix.
+  template <int D>
+  static __device__ __noinline__ Row fit(uint32_t o_at, uint32_t p_at, float f, int d, uint32_t ve) {
+    tmem_store_wait();
+    float top = 0.0f;
+#pragma unroll 1
+    for (int c = 0; c < D / 16; ++c) {
+      uint32_t v[16];
+      tmem_load16_now(o_at + 16 * c, v);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(__uint_as_float(v[i])));
+    }
+    top *= f;
+    const int delta = top > 0.0f ? max(0, max(int(__float_as_uint(top) >> 23) - 127 + d - 100, d - 126)) : 0;
+    if (__any_sync(0xffffffffu, delta > 0)) {
+      const float less = delta > 126 ? 0.0f : __uint_as_float(uint32_t(127 - delta) << 23);
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t p[16];
+        tmem_load16_now(p_at + 16 * c, p);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&p[i]));
+          const __half2 z = __floats2half2_rn(y.x * less, y.y * less);
+          p[i] = *reinterpret_cast<const uint32_t*>(&z);
+        }
+        tmem_store16(p_at + 16 * c, p);
+      }
+    }
+    return Row{0.0f, 0.0f, f * __uint_as_float(uint32_t(127 + min(126, max(-126, d - delta))) << 23), ve + uint32_t(delta)};
+  }
 
   __device__ __forceinline__ uint32_t seen(int c) const {  // of columns 32 c .. 32 c + 31
     const uint32_t e = c == 0 ? there.x : c == 1 ? there.y : c == 2 ? there.z : there.w;
@@ -763,7 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
       const int tok = mine ? row / t.group : 0;
       const int head = g.h * t.group + (mine ? row - tok * t.group : 0);
       float m = -INFINITY, l = 0.0f;
-      uint32_t ve = 0;  // exponent of the power of two that O is relative to
+      uint32_t ve = 0;  // exponent of the power of two that O is relative to; 0: none yet
       bool ok = true;
       if (f.js < f.je) {
         // the half's queries, a row's 16-byte pieces to their swizzled places
@@ -797,25 +915,42 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
           ++ns;
           fence_after();
           const uint4 there = *reinterpret_cast<const uint4*>(scp);
-          const uint32_t ve_before = j > f.js ? ve : 0;
-          ve = *reinterpret_cast<const uint32_t*>(scp + 20);
-          const float qu = qe * *reinterpret_cast<const float*>(scp + 16);
+          const uint32_t ve_before = ve;
+          uint4 power = *reinterpret_cast<const uint4*>(scp + 16);  // of keys and of values; whether a position has its own
+          if (F::HALVES == 2) power.w = power.z;                    // the same warps unpack both
+          const float qu = qe * __uint_as_float(power.x);
+          const bool apart = (power.z | power.w) != 0;
           const int64_t p0 = int64_t(j) * kKeys;
-          const bool full = p0 >= f.lo_max && p0 + kKeys <= f.hi_min && (there.x & there.y & there.z & there.w) == ~0u;
+          const bool full = !apart && p0 >= f.lo_max && p0 + kKeys <= f.hi_min && (there.x & there.y & there.z & there.w) == ~0u;
           // columns [c_lo, c_hi) are this row's
           const int c_lo = int(max(int64_t(0), min(int64_t(128), lo - p0)));
           const int c_hi = int(max(int64_t(0), min(int64_t(128), hi - p0)));
           float fix = 1.0f;
           const UnitSoftmax unit{s_at, s_at, there, c_lo, c_hi, qu};
-          if (full) unit.run<true>(m, l, fix);
-          else unit.run<false>(m, l, fix);
-          if (ve_before != 0 && ve != ve_before) fix *= __uint_as_float(uint32_t(max(0, 127 + int(ve_before) - int(ve))) << 23);
-          if (j > f.js && __any_sync(0xffffffffu, fix != 1.0f)) {
+          if (full) {
+            ve = power.y;
+            unit.run<true>(m, l, fix);
+          } else if (!apart) {
+            if (c_lo < c_hi) ve = power.y;  // a row that sees nothing here keeps its own
+            unit.run<false>(m, l, fix);
+          } else {
+            const UnitSoftmax::Row row = UnitSoftmax::run_apart(unit, smem + F::OWN + (kv & 3) * F::OWN_STAGE, qe,
+                                                                power, m, l, ve);
+            m = row.m, l = row.l, fix = row.fix, ve = row.ve;
+          }
+          const int finer = ve_before != 0 ? int(ve_before) - int(ve) : 0;
+          if (j > f.js && __any_sync(0xffffffffu, fix != 1.0f || finer != 0)) {
             // the product of the unit before has to be in O
             ok = mbar_wait(&bars->o[hf], (no - 1) & 1u);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             fence_after();
+            if (__any_sync(0xffffffffu, abs(finer) > 24)) {
+              const UnitSoftmax::Row row = UnitSoftmax::fit<D>(o_at, s_at, fix, finer, ve);
+              fix = row.fix, ve = row.ve;
+            } else {
+              fix *= __uint_as_float(uint32_t(127 + finer) << 23);
+            }
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
               uint32_t v[32], x[16];
@@ -946,7 +1081,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
         const int32_t* const pages = a.table + int64_t(w.seg().s) * a.ld_table;
         uint4 kr[CH], vr[CH];
         float ksc = 0.0f, vsc = 0.0f;
-        int vex = 0;  // exponent of the largest value scale that the segment's values are relative to
+        int vex = 0;  // exponent of the largest value scale that the unit's values are relative to
         bool in = false;
         // the page of this thread's position in unit j (-1: there is none), and its vector in that page
         auto page_of = [&](int j) {
@@ -984,19 +1119,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
         for (int j = ub; j < ue; ++j, ++kv) {
           const uint32_t st = kv % F::STAGES, round = kv / F::STAGES;
           const int page = page_of(j + 1);
-          ok = ok && !*abort && (round == 0 || mbar_wait(KEYS ? &bars->kempty[st] : &bars->vempty[st], (round - 1) & 1u));
-          ok = __all_sync(0xffffffffu, ok);
           // The scales are folded into the operands, with one rounding: a product
           // with a scale in two parts, hi and the rest.  Keys are relative to a
           // power of two of the unit's largest scale, so that fp16 holds them, values
-          // to one of the largest scale of the segment's first unit: a later unit
-          // whose scales are more than 2^3 times as large takes its own, and O is
-          // brought to it.  Codes times scales then stay below 2^15, and scales down to
-          // 2^-18 of the largest keep 11 bits (bf16 values cost the result 2^-8 of
-          // each, 0.0029 in place of 0.0017 in all).  A position whose scale is not
+          // to one of the largest scale of a unit before while that of this one is at most
+          // 2^3 times as large and no less than 2^-5 of it (else its own, and O is brought to
+          // it).  Codes times scales then stay below 2^15 and keep 11 bits down to
+          // 2^-kSpread (bf16 values cost the result 2^-8 of each, 0.0029 in place of 0.0017
+          // in all).  A position whose scale is smaller takes its own power of two, which
+          // the softmax multiplies in (UnitSoftmax::run_apart): else one large scale,
+          // hidden or not, would leave the others no digits.  A position whose scale is not
           // finite becomes NaN in its scores, and only there.
           uint32_t* const tops = reinterpret_cast<uint32_t*>(smem + F::TS + (kv & 1) * 32);
           uint8_t* const scp = smem + F::SC + (kv & 3) * F::SC_STAGE;
+          uint8_t* const apart = scp + (KEYS ? 24 : 28) + (warp & 3);  // whether a position of this warp's is
           const bool k_fine = (__float_as_uint(ksc) & 0x7f800000u) != 0x7f800000u;
           const bool v_fine = (__float_as_uint(vsc) & 0x7f800000u) != 0x7f800000u;
           {
@@ -1004,40 +1140,58 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
             const uint32_t vtop = VALUES ? __reduce_max_sync(0xffffffffu, v_fine ? __float_as_uint(vsc) & 0x7fffffffu : 0u) : 0u;
             const uint32_t b = __ballot_sync(0xffffffffu, in);
             if (lane == 0) {
+              *apart = 0;
               if (KEYS) tops[warp & 3] = ok ? top : kFailed, reinterpret_cast<uint32_t*>(scp)[warp & 3] = b;
               if (VALUES) tops[4 + (warp & 3)] = ok ? vtop : kFailed;
             }
           }
           meet();
-          float down = 0.0f;
+          int kex = 0;  // exponent of the unit's largest key scale
           if constexpr (KEYS) {
             const uint4 all = *reinterpret_cast<const uint4*>(tops);
-            const uint32_t ex = max(1u, max(max(all.x, all.y), max(all.z, all.w)) >> 23);
-            told = ex > 255;
-            down = __uint_as_float(ex == 254 ? 0x00400000u : (254 - ex) << 23);
-            if (i == 0) *reinterpret_cast<uint32_t*>(scp + 16) = ex << 23;
+            kex = int(max(1u, max(max(all.x, all.y), max(all.z, all.w)) >> 23));
+            told = kex > 255;
+            if (i == 0) *reinterpret_cast<uint32_t*>(scp + 16) = uint32_t(kex) << 23;
           }
           if constexpr (VALUES) {
             const uint4 all = *reinterpret_cast<const uint4*>(tops + 4);
             const uint32_t vtop = max(max(all.x, all.y), max(all.z, all.w)) >> 23;
             told = vtop > 255;
-            const int vx = min(250, max(8, int(vtop)));
-            if (j == ub || vx > vex + 3) vex = vx;
+            const int vx = max(8, int(vtop));
+            if (j == ub || vx > vex + 3 || (vtop != 0 && vx < vex - 5)) vex = vx;
             if (i == 0) *reinterpret_cast<uint32_t*>(scp + 20) = uint32_t(vex - kValueBits);
           }
           if (told) break;
-          mbar_arrive(&bars->sc[kv & 3]);
+          const int k_own = int(__float_as_uint(ksc) >> 23) & 255, v_own = int(__float_as_uint(vsc) >> 23) & 255;
+          const bool k_apart = KEYS && k_own + kSpread < kex && ksc != 0.0f;
+          const bool v_apart = VALUES && v_own + kSpread < vex && vsc != 0.0f;
+          const int ke = k_apart ? max(1, k_own) : kex, ve = v_apart ? max(1, v_own) : vex - kValueBits;
           uint32_t k_hi, k_lo, v_hi, v_lo;
           {
-            const float sc = v_fine ? ksc * down : __uint_as_float(0x7fc00000u);
+            auto inverse = [](int e) { return __uint_as_float(e == 254 ? 0x00400000u : uint32_t(254 - e) << 23); };
+            const float sc = v_fine ? ksc * inverse(ke) : __uint_as_float(0x7fc00000u);
             const __half hi = __float2half_rn(sc), lo = __float2half_rn(sc - __half2float(hi));
             k_hi = uint32_t(__half_as_ushort(hi)) * 0x10001u;
             k_lo = uint32_t(__half_as_ushort(lo)) * 0x10001u;
-            const float vz = v_fine ? vsc * __uint_as_float(uint32_t(254 + kValueBits - vex) << 23) : 0.0f;
+            const float vz = v_fine ? vsc * inverse(ve) : 0.0f;
             const __half vh = __float2half_rn(vz), vl = __float2half_rn(vz - __half2float(vh));
             v_hi = uint32_t(__half_as_ushort(vh)) * 0x10001u;
             v_lo = uint32_t(__half_as_ushort(vl)) * 0x10001u;
           }
+          // tells the softmax; the rings of four units are free here, as it is done with the unit
+          // before the one that the last wait was for
+          auto tell = [&]() {
+            if (__any_sync(0xffffffffu, k_apart || v_apart)) {
+              uint8_t* const own = smem + F::OWN + (kv & 3) * F::OWN_STAGE + i;
+              if (KEYS) own[0] = k_apart ? uint8_t(ke) : 0;
+              if (VALUES) own[kKeys] = v_apart ? uint8_t(ve) : 0;
+              if (lane == 0) *apart = 1;
+            }
+            mbar_arrive(&bars->sc[kv & 3]);
+          };
+          if constexpr (!KEYS) tell();
+          ok = ok && !*abort && (round == 0 || mbar_wait(KEYS ? &bars->kempty[st] : &bars->vempty[st], (round - 1) & 1u));
+          ok = __all_sync(0xffffffffu, ok);
           auto store = [&](uint8_t* tile, const uint4 (&x)[CH], uint32_t s_hi, uint32_t s_lo) {
             uint8_t* row = tile + i * 128;
             const int turn = i & 7;
@@ -1063,6 +1217,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
           };
           if constexpr (KEYS) {
             store(smem + F::K + st * F::TILE, kr, k_hi, k_lo);
+            tell();
             fence_proxy_async_smem();
             mbar_arrive(&bars->kfull[st]);
           }
