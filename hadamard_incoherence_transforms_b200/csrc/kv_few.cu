@@ -13,7 +13,10 @@
 //     the offset -- exact; the query is scaled to [-2, 2) by a power of two of
 //     its own row, so that fp16 holds it to 2^-11 whatever its size;
 //   V to fp16 likewise; the other operand, probability times the value's scale, is
-//     rounded to fp16, the scale relative to a power of two that each warp keeps.
+//     rounded to fp16.
+// What a row's sums are relative to follows that product (the base-2 score plus the logarithm
+// of the value's scale), so that fp16 holds the ones that make up the result, whatever
+// the scales of positions that the row does not see or gives no weight.
 // O^T += V^T P^T takes P^T from the score accumulators with one 8x8 transpose
 // per 8 positions.  Scales never touch the codes: the key's multiplies its
 // score, the value's its probability.
@@ -37,8 +40,11 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStages = 3;
-constexpr float kGrow = 2048.0f;  // a lane's share of a column's sum above which it gets a new reference
-constexpr float kRoom = 4.0f;     // a reference's own probability is 2^kRoom
+constexpr float kGrow = 32768.0f;  // bound of a column's products above which it gets a new reference
+constexpr float kRoom = 4.0f;      // the largest product is 2^kRoom with a new reference
+// A reference stays within 2^kFar of the largest probability, and a lane's share of a column's
+// sum below kFull, so that fp32 holds the sum where the values are next to nothing.
+constexpr float kFar = 90.0f, kFull = 1.2676506e30f;  // 2^100
 constexpr int kLead = 16;  // beginning a pair takes a CTA about as long as 16 units
 
 // Positions of a unit: stages of 2 to 4 KB (8 KB for heads of 256); three of
@@ -353,7 +359,6 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
       m[n][1] = 8 * n + 2 * c4 + 1 < nr ? -INFINITY : 0.0f;
       l[n][0] = l[n][1] = 0.0f;
     }
-    int ve = -200;  // exponent of the power of two that o is relative to; none yet
     int stage = 0;
     for (int i = 0; i < nu; ++i) {
       issue();
@@ -430,9 +435,9 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
           }
       }
 
-      // Probabilities against the columns' references so far.  A reference is a
-      // maximum of scores seen before, less kRoom, and is only raised where a lane's
-      // share of a column adds up to more than kGrow.
+      // Probabilities against the columns' references so far, and a bound of their products
+      // with the values' scales.  A reference is a maximum of products seen before (as
+      // logarithms), less kRoom, and is only raised where the bound exceeds kGrow.
       float pr[MT][NT][4], add[NT][2];
       auto powers = [&]() {
 #pragma unroll
@@ -449,28 +454,47 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
         }
       };
       powers();
+      uint32_t big = __float_as_uint(vs[lane & (TK - 1)]) & 0x7fffffffu;
+      if (!full) {  // of positions that a row of the tile sees: others hold anything
+        const int64_t p = p0 + (lane & (TK - 1));
+        if (!((there >> (lane & (TK - 1))) & 1) || p < lo_min || p >= hi_max) big = 0;
+      }
+      if (big >= 0x7f800000u) big = 0;
+      const float largest = __uint_as_float(__reduce_max_sync(0xffffffffu, big));
       bool grow = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) grow |= m[n][k] == -INFINITY || add[n][k] > kGrow;
+        for (int k = 0; k < 2; ++k) grow |= m[n][k] == -INFINITY || add[n][k] * largest > kGrow || add[n][k] > kFull;
       if (__any_sync(0xffffffffu, grow)) {
+        float lv[MT][2];  // the values' scales as logarithms
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          lv[mt][0] = __log2f(vs[16 * mt + r8]);
+          lv[mt][1] = __log2f(vs[16 * mt + r8 + 8]);
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float f[2];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            float v = -INFINITY;
+            float v = -INFINITY, w = -INFINITY;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) v = fmaxf(v, fmaxf(sc[mt][n][k], sc[mt][n][k + 2]));
-            v *= qe[n][k];
+            for (int mt = 0; mt < MT; ++mt) {
+              const float x0 = sc[mt][n][k] * qe[n][k], x1 = sc[mt][n][k + 2] * qe[n][k];
+              v = fmaxf(v, fmaxf(x0, x1));
+              w = fmaxf(w, fmaxf(x0 == -INFINITY ? x0 : x0 + lv[mt][0], x1 == -INFINITY ? x1 : x1 + lv[mt][1]));
+            }
+            v = fmaxf(w, v - kFar);
 #pragma unroll
             for (int b = 4; b < 32; b <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, b));
             // a column's lanes agree on v, and so on its new reference
             v -= kRoom;
-            f[k] = v > m[n][k] ? ex2(m[n][k] - v) : 1.0f;
+            // in two halves: the sum of probabilities outlives a step of more than 2^126
+            const float half = v > m[n][k] ? ex2(0.5f * (m[n][k] - v)) : 1.0f;
             m[n][k] = fmaxf(m[n][k], v);
-            l[n][k] *= f[k];
+            f[k] = half * half;
+            l[n][k] = l[n][k] * half * half;
           }
 #pragma unroll
           for (int d = 0; d < OM; ++d)
@@ -479,35 +503,15 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
         }
         powers();
       }
-      // Values' scales relative to a power of two: that of the largest one so far, or
-      // up to 2^3 below it.  Probability times scale is then below 2^15, and fp16 keeps 11
-      // bits of it down to 2^-18 of the largest (bf16 kept 8: an error of 0.0024 of the
-      // result in place of 0.0017; 80 us in place of 84 with 4 bits, 75 of 70 with 8).
-      uint32_t big = __float_as_uint(vs[lane & (TK - 1)]) & 0x7fffffffu;
-      if (!full) {  // of positions that a row of the tile sees: others hold anything
-        const int64_t p = p0 + (lane & (TK - 1));
-        if (!((there >> (lane & (TK - 1))) & 1) || p < lo_min || p >= hi_max) big = 0;
-      }
-      if (big >= 0x7f800000u) big = 0;
-      const int ex = min(250, max(8, int(__reduce_max_sync(0xffffffffu, big) >> 23)));
-      if (ex > ve + 3) {
-        const float f = __uint_as_float(uint32_t(max(0, 127 + ve - ex)) << 23);
-#pragma unroll
-        for (int d = 0; d < OM; ++d)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[d][n][e] *= f;
-        ve = ex;
-      }
-      const float vdown = __uint_as_float(uint32_t(254 - ve) << 23);
+      // fp16 keeps 11 bits of a product down to 2^-18 of the largest (bf16 kept 8: an error
+      // of 0.0024 of the result in place of 0.0017).
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         l[n][0] += add[n][0];
         l[n][1] += add[n][1];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          const float v0 = vs[16 * mt + r8] * vdown, v1 = vs[16 * mt + r8 + 8] * vdown;
+          const float v0 = vs[16 * mt + r8], v1 = vs[16 * mt + r8 + 8];
 #pragma unroll
           for (int e = 0; e < 4; ++e) pr[mt][n][e] *= e < 2 ? v0 : v1;
         }
@@ -563,7 +567,6 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
     __syncthreads();
 
     // join the warps; shared memory is free now
-    const float up = __uint_as_float(uint32_t(max(0, ve)) << 23);
     float* mo = reinterpret_cast<float*>(smem);                       // [kWarps][ROWS][D]
     float2* ms = reinterpret_cast<float2*>(mo + kWarps * ROWS * D);   // [kWarps][ROWS]
     static_assert(kWarps * ROWS * (D * 4 + 8) <= kStages * kWarps * F::STAGE, "join buffer");
@@ -580,11 +583,11 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
 #pragma unroll
           for (int x = 0; x < CH; ++x)
             *reinterpret_cast<float4*>(dst + 32 * x + 4 * r8) =
-                make_float4(o[2 * x][n][k] * up, o[2 * x][n][k + 2] * up, o[2 * x + 1][n][k] * up, o[2 * x + 1][n][k + 2] * up);
+                make_float4(o[2 * x][n][k], o[2 * x][n][k + 2], o[2 * x + 1][n][k], o[2 * x + 1][n][k + 2]);
         } else {  // tile x: elements 16 x + 2 r8, + 1
 #pragma unroll
           for (int x = 0; x < CH; ++x)
-            *reinterpret_cast<float2*>(dst + 16 * x + 2 * r8) = make_float2(o[x][n][k] * up, o[x][n][k + 2] * up);
+            *reinterpret_cast<float2*>(dst + 16 * x + 2 * r8) = make_float2(o[x][n][k], o[x][n][k + 2]);
         }
       }
     }
@@ -602,8 +605,8 @@ __global__ void __launch_bounds__(kThreads, MINB) k_kv_few(const KvArgs a, const
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float2 v = ms[w * ROWS + r];
-        const float g = kv_weight(v.x, top);
-        sum = fmaf(g, v.y, sum);
+        const float half = kv_weight(v.x, top), g = half * half;
+        sum = fmaf(v.y * half, half, sum);
 #pragma unroll
         for (int e = 0; e < E; ++e) x[e] = fmaf(g, mo[(w * ROWS + r) * D + E * lane + e], x[e]);
       }

@@ -188,9 +188,10 @@ __device__ __forceinline__ void kv_finish(float (&x)[D / 32], const KvArgs& a, c
   }
 }
 
-// Weight of a part with maximum m below the joint maximum top (base 2); a NaN
-// maximum or sum stays NaN.
-__device__ __forceinline__ float kv_weight(float m, float top) { return m == -INFINITY ? 0.0f : exp2f(m - top); }
+// Square root of the weight of a part with reference m below the joint one, top (base 2); a NaN
+// reference or sum stays NaN.  Taken twice, so that a part's sum outlives a weight below
+// 2^-126: references follow the values' sizes too.
+__device__ __forceinline__ float kv_weight(float m, float top) { return m == -INFINITY ? 0.0f : exp2f(0.5f * (m - top)); }
 // max that keeps a NaN
 __device__ __forceinline__ float kv_max(float a, float b) {
   float r;
@@ -238,11 +239,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_kv_join(const KvArgs a, con
       for (int j0 = 0; j0 < count; j0 += 32) {
         const float2 q = j0 + lane < count ? w.ms[place(j0 + lane)] : make_float2(-INFINITY, 0.0f);
         const float mine = kv_weight(q.x, m);
-        l = fmaf(mine, q.y, l);
+        l = fmaf(q.y * mine, mine, l);
         const int n = min(32, count - j0);
 #pragma unroll 8
         for (int j = 0; j < n; ++j) {
-          const float f = __shfl_sync(0xffffffffu, mine, j);
+          const float half = __shfl_sync(0xffffffffu, mine, j), f = half * half;
           const float* src = w.rows + place(j0 + j) * D + E * lane;
           float v[E];
           if constexpr (E == 2) {
@@ -270,13 +271,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_kv_join(const KvArgs a, con
       if (team == 0) {
         float top = m;
         for (int i = 1; i < teams; ++i) top = kv_max(top, sm[warp + i * per]);
-        const float f0 = kv_weight(m, top);
-        l *= f0;
+        const float half0 = kv_weight(m, top), f0 = half0 * half0;
+        l = l * half0 * half0;
 #pragma unroll
         for (int e = 0; e < E; ++e) x[e] *= f0;
         for (int i = 1; i < teams; ++i) {
-          const float f = kv_weight(sm[warp + i * per], top);
-          l = fmaf(f, sl[warp + i * per], l);
+          const float half = kv_weight(sm[warp + i * per], top), f = half * half;
+          l = fmaf(sl[warp + i * per] * half, half, l);
 #pragma unroll
           for (int e = 0; e < E; ++e) x[e] = fmaf(f, sx[warp + i * per][E * lane + e], x[e]);
         }

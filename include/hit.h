@@ -406,13 +406,13 @@ HIT_API int harp_blocks(const float* theta, const int8_t* theta_q, float theta_s
  *   power of two of their own row) fp16, scores and outputs summed in fp32,
  *   softmax in fp32.  Where a sequence has at most 64 query rows (tokens * heads
  *   / kv_heads; 32 with head_dim 256) for a key/value head, codes and the keys'
- *   scales enter exactly and probabilities times the values' scales in fp16,
- *   relative to the largest scale of the positions before theirs and of their
- *   block of up to 32: 11 bits of what is not below 2^-18 of it.  In longer
- *   chunks keys, probabilities and values are each rounded to fp16, behind powers
- *   of two that are a position's own wherever scales lie far apart: 11 bits of a
- *   key, of a value and of a probability not below 2^-18 of its row's largest,
- *   whatever the scales of positions that the row does not see or gives no weight.  Two calls
+ *   scales enter exactly and the product of a probability and the value's scale
+ *   in fp16: 11 bits of what is not below 2^-18 of its row's largest (for scales
+ *   of 2^-100 to 2^100).  In longer chunks keys, probabilities and values are each
+ *   rounded to fp16, behind powers of two that are a position's own wherever scales
+ *   lie far apart: 11 bits of a key, of a value and of a probability not below
+ *   2^-18 of its row's largest.  Positions that a row does not see cost it nothing,
+ *   whatever they hold.  Two calls
  *   on the same inputs give the same bits.
  *   max_new: an upper bound of n_s (any value >= 1 gives right results; a tight
  *   one saves launches and workspace).  Needs rht_kv_workspace_bytes(tokens,

@@ -68,7 +68,7 @@ def run(c, new, g, window=0, q64=None):
     return hit.rht_kv_attention(q, *c.on(), torch.from_numpy(cu).cuda(), **c.signs(), window=window), ref
 
 
-ROWS = [(100, 2), (65, 1)]  # new tokens, query heads of a key head: more than 64 rows
+ROWS = [(100, 2), (65, 1), (1, 4), (4, 4)]  # new tokens, query heads of a key head: more than 64 rows, and few
 SIZES = [(64, 8), (128, 4), (256, 8), (256, 4)]
 
 
@@ -94,6 +94,16 @@ def test_prompts_do_not_see_later_tokens(d, bits, left, which):
         set_scale(c, w, 0, range(238, 250), left)
     got, ref = run(c, [200], 1)
     check_rows(got, ref, np.arange(238 - 50), 250)
+
+
+@pytest.mark.parametrize("d,bits", SIZES)
+@pytest.mark.parametrize("left", [1e30, 1e-30])
+def test_drafted_tokens_do_not_see_later_ones(d, bits, left):
+    c = Cache(85, [300], 1, d, bits, 16).fill()
+    for w in (0, 1):
+        set_scale(c, w, 0, [299], left)
+    got, ref = run(c, [4], 4)
+    check_rows(got, ref, np.arange(3), 300)
 
 
 @pytest.mark.parametrize("new,g", ROWS)
