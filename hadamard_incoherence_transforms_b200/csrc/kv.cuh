@@ -4,6 +4,7 @@
 #pragma once
 #include "device.cuh"
 #include "kv.h"
+#include "kv_turn.h"
 
 namespace hit {
 
@@ -121,7 +122,7 @@ __device__ __forceinline__ int kv_turn_pos(const KvArgs& a, int64_t t, int pos, 
 }
 // Twice the angle's fraction of a turn, in [-1, 1].
 __device__ __forceinline__ float kv_halfturns(int pos, uint64_t turn) {
-  return float(int(uint64_t(int64_t(pos) * int64_t(turn)) >> 32)) * 4.656612873077393e-10f;
+  return float(kv_fraction(pos, turn)) * 4.656612873077393e-10f;
 }
 // (cos, sin) to fp32's precision, for keys.
 __device__ __forceinline__ float2 kv_angle(const KvArgs& a, const uint64_t* turns, int64_t t, int pos, int j) {
@@ -129,8 +130,9 @@ __device__ __forceinline__ float2 kv_angle(const KvArgs& a, const uint64_t* turn
   sincospif(kv_halfturns(kv_turn_pos(a, t, pos, j), turns[j]), &s, &c);
   return make_float2(c, s);
 }
-// The same to 2^-21 by the hardware's functions, for queries, which are rounded
-// to 2^-11 after their turn.
+// The same to an absolute error below 2^-19 by the hardware's functions (2^-21.2 on this
+// range, the argument's roundings as much again), for queries, which are rounded to
+// 2^-11 after their turn.
 __device__ __forceinline__ float2 kv_angle_fast(const KvArgs& a, const uint64_t* turns, int64_t t, int pos, int j) {
   const float x = kv_halfturns(kv_turn_pos(a, t, pos, j), turns[j]) * 3.14159265358979f;
   return make_float2(__cosf(x), __sinf(x));

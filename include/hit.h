@@ -382,8 +382,10 @@ HIT_API int harp_blocks(const float* theta, const int8_t* theta_q, float theta_s
  *    NULL for +1.
  *  - inv_freq: fp32 [n_freq], rotary position frequencies applied to keys and
  *    queries (not values) before the rotation, or NULL (n_freq 0).  The angle
- *    of pair j is pos * inv_freq[j], evaluated in fp64 before its sine and
- *    cosine are taken in fp32; (x, y) becomes (x cos - y sin, x sin + y cos).
+ *    of pair j is pos * inv_freq[j]: the frequency's fraction of a turn is found in
+ *    fp64, its product with the position is exact modulo a turn, so that far
+ *    positions keep their digits.  Sine and cosine are fp32's for keys, and within
+ *    2^-19 for queries; (x, y) becomes (x cos - y sin, x sin + y cos).
  *    Pairs are (j, j + n_freq), n_freq a multiple of 8, or with interleaved
  *    != 0 (2j, 2j + 1), n_freq a multiple of 4; 2 n_freq <= head_dim, elements
  *    from 2 n_freq on are not turned.
