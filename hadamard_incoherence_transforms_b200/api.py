@@ -411,6 +411,7 @@ def butterfly_apply_tc(x, radices, blocks, axis: int = 1, transpose: bool = Fals
 # Rotated key/value cache
 # ---------------------------------------------------------------------------
 _KV = struct.Struct("@12Q4q8i")  # struct hit_kv
+_KV_ZERO = 0x100  # HIT_KV_ZERO
 
 
 def kv_cache_shapes(pages: int, page_size: int, kv_heads: int, head_dim: int, bits: int):
@@ -561,11 +562,13 @@ def rht_kv_attention(q, k_codes, k_scales, v_codes, v_scales, page_table, lens, 
 
     q is turned and rotated as the keys were; the result is rotated back.  A token at position p sees the cached
     positions up to p (all of them with causal=False; the last `window` ones with window > 0).  max_new bounds the
-    tokens of one sequence (default: all of them).  out may be float32 or bfloat16 (default: q's type)."""
+    tokens of one sequence (default: all of them).  out may be float32 or bfloat16 (default: q's type).  Rows of tokens
+    that belong to no sequence (before cu[0], from cu[-1] on) are zero, or as they were where out is given."""
     _kv_dense(q, "q")
     dev, (n, heads, d) = q.get_device(), q.shape
+    zero = 0
     if out is None:
-        out = _kv_empty(n, heads, d, q.dtype, q.device)
+        out, zero = _kv_empty(n, heads, d, q.dtype, q.device), _KV_ZERO
     else:
         _kv_dense(out, "out")
         if out.shape != q.shape or out.get_device() != dev:
@@ -583,7 +586,7 @@ def rht_kv_attention(q, k_codes, k_scales, v_codes, v_scales, page_table, lens, 
     q_ts, q_hs, _ = q.stride()
     o_ts, o_hs, _ = out.stride()
     _kv_call(dev, "rht_kv_attention", kv, q.data_ptr(), out.data_ptr(), n, heads, q_ts, q_hs, o_ts, o_hs, _dt(q.dtype),
-             _dt(out.dtype), float(d ** -0.5 if sm_scale is None else sm_scale), int(bool(causal)), int(window), max_new,
+             _dt(out.dtype) | zero, float(d ** -0.5 if sm_scale is None else sm_scale), int(bool(causal)), int(window), max_new,
              workspace.data_ptr(), size)
     return out
 
@@ -592,20 +595,25 @@ def rht_kv_read(k_codes, k_scales, v_codes, v_scales, page_table, lens, cu, rows
                 v_signs=None, out_dtype=torch.bfloat16, k_out=None, v_out=None):
     """What the cache stands for at the call's tokens: (k, v), each [rows, kv_heads, head_dim], rotated back.
 
-    Sequence s owns rows cu[s] .. cu[s + 1], the last of its lens[s] positions; keys keep their rotary turn."""
+    Sequence s owns rows cu[s] .. cu[s + 1], the last of its lens[s] positions; keys keep their rotary turn.  Rows of no
+    sequence are zero, or as they were in a k_out or v_out that is given."""
     dev, hk = _cuda(k_codes, "k_codes").get_device(), k_codes.shape[1]
     if k_out is not None:
         out_dtype = k_out.dtype
     elif v_out is not None:
         out_dtype = v_out.dtype
-    k = _kv_empty(rows, hk, head_dim, out_dtype, k_codes.device) if k_out is None else _kv_dense(k_out, "k_out")
-    v = _kv_empty(rows, hk, head_dim, out_dtype, k_codes.device) if v_out is None else _kv_dense(v_out, "v_out")
-    if k_out is not None or v_out is not None:
+    if k_out is None and v_out is None:
+        k, v = (_kv_empty(rows, hk, head_dim, out_dtype, k_codes.device) for _ in range(2))
+        zero = _KV_ZERO
+    else:
         shape = (rows, hk, head_dim)
+        k = torch.zeros(shape, dtype=out_dtype, device=k_codes.device) if k_out is None else _kv_dense(k_out, "k_out")
+        v = torch.zeros(shape, dtype=out_dtype, device=k_codes.device) if v_out is None else _kv_dense(v_out, "v_out")
+        zero = 0
         if k.shape != shape or v.shape != shape or k.dtype != v.dtype or k.get_device() != dev or v.get_device() != dev:
             raise ValueError("k_out and v_out must be [rows, kv_heads, head_dim] of one dtype on the cache's device")
     kv = _kv(head_dim, dev, rows, k_codes, k_scales, v_codes, v_scales, page_table, lens, cu, k_signs, v_signs)
     k_ts, k_hs, _ = k.stride()
     v_ts, v_hs, _ = v.stride()
-    _kv_call(dev, "rht_kv_read", kv, k.data_ptr(), v.data_ptr(), rows, k_ts, k_hs, v_ts, v_hs, _dt(out_dtype))
+    _kv_call(dev, "rht_kv_read", kv, k.data_ptr(), v.data_ptr(), rows, k_ts, k_hs, v_ts, v_hs, _dt(out_dtype) | zero)
     return k, v

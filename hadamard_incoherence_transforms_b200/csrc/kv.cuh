@@ -230,6 +230,22 @@ __device__ __forceinline__ void kv_store8(void* p, int64_t at, const float* x) {
   }
 }
 
+// Zeros in the rows of tokens [0, lo) and [hi, tokens) of out, 16 bytes a thread;
+// thread: this one's number among `threads`.
+__device__ __forceinline__ void kv_zero_rows(void* out, int64_t lo, int64_t hi, int64_t tokens, int heads, int row_bytes,
+                                             int64_t token_bytes, int64_t head_bytes, int64_t thread, int64_t threads) {
+  lo = max(int64_t(0), min(lo, tokens));
+  hi = max(lo, min(hi, tokens));
+  const int pieces = row_bytes / 16;
+  const int64_t of_token = int64_t(heads) * pieces, n = (lo + tokens - hi) * of_token;
+  for (int64_t i = thread; i < n; i += threads) {
+    const int64_t r = i / of_token, t = r < lo ? r : r - lo + hi;
+    const int in = int(i - r * of_token), h = in / pieces;
+    uint8_t* const p = static_cast<uint8_t*>(out) + t * token_bytes + h * head_bytes + (in - h * pieces) * 16;
+    *reinterpret_cast<uint4*>(p) = make_uint4(0, 0, 0, 0);
+  }
+}
+
 // The rotary turn of a vector whose elements start at p + at; cs holds the
 // token's (cos, sin) pairs.
 template <int D, bool F32>

@@ -34,7 +34,11 @@ struct KvDense {
   int64_t k_ts = 0, k_hs = 0, v_ts = 0, v_hs = 0;
 };
 cudaError_t launch_kv_append(const KvArgs& a, const KvDense& x, int dt, cudaStream_t st);
-cudaError_t launch_kv_read(const KvArgs& a, const KvDense& y, int dt, cudaStream_t st);
+// zero: rows of tokens that belong to no sequence are set to zero
+cudaError_t launch_kv_read(const KvArgs& a, const KvDense& y, int dt, bool zero, cudaStream_t st);
+// All rows [tokens, heads, head_dim] of out.
+cudaError_t launch_kv_zero(void* out, int64_t tokens, int heads, int head_dim, int64_t ts, int64_t hs, int dt,
+                           cudaStream_t st);
 
 struct KvAttn {
   const void* q = nullptr;
@@ -43,6 +47,7 @@ struct KvAttn {
   int heads = 0, group = 1;  // query heads; of one key/value head
   int q_f32 = 0, o_f32 = 0, causal = 1;
   int wide = 0;  // every row of out starts on a 32-byte boundary
+  int zero = 0;  // the launch sets the rows of tokens that belong to no sequence to zero
   int64_t rows_lo = 0, rows_hi = INT64_MAX;  // sequences with this many query rows (token * group) belong to the launch
   float scale = 1.0f;
   int64_t window = 0;

@@ -149,11 +149,13 @@ int rht_kv_append(const hit_kv* kv, const void* k, const void* v, int64_t tokens
 int rht_kv_read(const hit_kv* kv, void* k, void* v, int64_t rows, int64_t k_ts, int64_t k_hs, int64_t v_ts, int64_t v_hs,
                 int dtype, void* stream) {
   const char* fn = "rht_kv_read";
+  const bool zero = (dtype & HIT_KV_ZERO) != 0;
+  dtype &= ~HIT_KV_ZERO;
   if (dtype != HIT_F32 && dtype != HIT_BF16) return fail(HIT_EUNSUPPORTED, "%s: unknown dtype", fn);
   hit::KvArgs a;
   int r = check_kv(fn, kv, rows, false, a);
   if (r) return r;
-  if (rows == 0 || a.seqs == 0 || (k == nullptr && v == nullptr)) return HIT_OK;
+  if (rows == 0 || (a.seqs == 0 && !zero) || (k == nullptr && v == nullptr)) return HIT_OK;
   if (k != nullptr && (r = check_dense(fn, "k", k, k_ts, k_hs, dtype)) != 0) return r;
   if (v != nullptr && (r = check_dense(fn, "v", v, v_ts, v_hs, dtype)) != 0) return r;
   hit::KvDense y;
@@ -163,7 +165,14 @@ int rht_kv_read(const hit_kv* kv, void* k, void* v, int64_t rows, int64_t k_ts, 
   y.k_hs = k_hs;
   y.v_ts = v_ts;
   y.v_hs = v_hs;
-  return cuda_status(hit::launch_kv_read(a, y, dtype, static_cast<cudaStream_t>(stream)), fn);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (a.seqs == 0) {
+    cudaError_t e = cudaSuccess;
+    if (k != nullptr) e = hit::launch_kv_zero(k, rows, a.hk, a.head_dim, k_ts, k_hs, dtype, st);
+    if (v != nullptr && e == cudaSuccess) e = hit::launch_kv_zero(v, rows, a.hk, a.head_dim, v_ts, v_hs, dtype, st);
+    return cuda_status(e, fn);
+  }
+  return cuda_status(hit::launch_kv_read(a, y, dtype, zero, st), fn);
 }
 
 size_t rht_kv_workspace_bytes(int64_t tokens, int heads, int kv_heads, int head_dim, int64_t max_new) {
@@ -179,6 +188,8 @@ int rht_kv_attention(const hit_kv* kv, const void* q, void* out, int64_t tokens,
                      int64_t o_ts, int64_t o_hs, int dtype_q, int dtype_out, float sm_scale, int causal, int64_t window,
                      int64_t max_new, void* workspace, size_t workspace_bytes, void* stream) {
   const char* fn = "rht_kv_attention";
+  const bool zero = (dtype_out & HIT_KV_ZERO) != 0;
+  dtype_out &= ~HIT_KV_ZERO;
   if ((dtype_q != HIT_F32 && dtype_q != HIT_BF16) || (dtype_out != HIT_F32 && dtype_out != HIT_BF16))
     return fail(HIT_EUNSUPPORTED, "%s: unknown dtype", fn);
   hit::KvArgs a;
@@ -189,12 +200,14 @@ int rht_kv_attention(const hit_kv* kv, const void* q, void* out, int64_t tokens,
   if (!std::isfinite(sm_scale)) return fail(HIT_EINVAL, "%s: sm_scale must be finite", fn);
   if (window < 0 || (window > 0 && !causal)) return fail(HIT_EINVAL, "%s: a window must be positive and causal", fn);
   if (max_new < 1) return fail(HIT_EINVAL, "%s: max_new must be positive", fn);
-  if (tokens == 0 || a.seqs == 0) return HIT_OK;
+  if (tokens == 0 || (a.seqs == 0 && !zero)) return HIT_OK;
   if (tokens * heads >= kMaxTokens) return fail(HIT_EUNSUPPORTED, "%s: tokens * heads must stay below 2^31", fn);
   r = check_dense(fn, "q", q, q_ts, q_hs, dtype_q);
   if (r) return r;
   r = check_dense(fn, "out", out, o_ts, o_hs, dtype_out);
   if (r) return r;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (a.seqs == 0) return cuda_status(hit::launch_kv_zero(out, tokens, heads, a.head_dim, o_ts, o_hs, dtype_out, st), fn);
   const size_t need = rht_kv_workspace_bytes(tokens, heads, a.hk, a.head_dim, max_new);
   if (need > 0) {
     if (workspace == nullptr || workspace_bytes < need)
@@ -214,16 +227,17 @@ int rht_kv_attention(const hit_kv* kv, const void* q, void* out, int64_t tokens,
   t.o_f32 = dtype_out == HIT_F32;
   const int64_t out_bytes = t.o_f32 ? 4 : 2;
   t.wide = aligned(out, 32) && o_ts * out_bytes % 32 == 0 && o_hs * out_bytes % 32 == 0;
+  t.zero = zero ? 1 : 0;
   t.causal = causal ? 1 : 0;
   t.scale = sm_scale;
   t.window = window;
   t.max_new = max_new < tokens ? max_new : tokens;
   t.ws = workspace;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (few_only(t.max_new, t.group, a.head_dim)) return cuda_status(hit::launch_kv_few(a, t, st), fn);
   hit::KvAttn few = t;
   few.rows_hi = few.max_new = few_rows(a.head_dim);
   t.rows_lo = few.rows_hi + 1;
+  t.zero = 0;  // few's part
   r = cuda_status(hit::launch_kv_prompt_queries(a, t, st), fn);
   if (r == HIT_OK) r = cuda_status(hit::launch_kv_few(a, few, st), fn);
   return r ? r : cuda_status(hit::launch_kv_prompt(a, t, st), fn);

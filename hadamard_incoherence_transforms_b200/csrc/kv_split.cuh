@@ -213,6 +213,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_kv_join(const KvArgs a, con
   const KvWork w = kv_work_of<D, ROWS>(t.ws, ctas);
   const int c = blockIdx.x, first_row = blockIdx.y * PER;
   const KvPart p = w.part[2 * c + 1];
+  if (t.zero) {
+    const int es = t.o_f32 ? 4 : 2;
+    kv_zero_rows(t.out, __ldg(a.cu), __ldg(a.cu + a.seqs), a.tokens, t.heads, D * es, t.o_ts * es, t.o_hs * es,
+                 (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x,
+                 int64_t(gridDim.x) * gridDim.y * blockDim.x);
+  }
   if (p.first < 0 || first_row >= p.rows) return;
   const int rows = min(PER, p.rows - first_row);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) k_kv_append(const KvArg
 // numbered such that a lane ends with D / 4 neighbouring elements of its rows.
 template <int D, int BITS, bool F32>
 __global__ void __launch_bounds__(kThreads, kReadCtas) k_kv_read(const KvArgs a, const KvDense y, int tile, float norm,
-                                                                 int wide, FastDiv by_heads) {
+                                                                 int wide, int zero, FastDiv by_heads) {
   constexpr int VB = D * BITS / 8, NW = VB / 16;  // a lane's words of a vector's codes
   constexpr int NP = D / 8;                       // ... and its fp16 pairs
   __shared__ Tile tl;
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, kReadCtas) k_kv_read(const KvArgs a,
       if (v >= vectors || !wanted) continue;
       const int j = div_by(v, by_heads), h = v - j * a.hk;
       const int64_t slot = tl.slot[j];
-      row[k].owned = slot != kNone;
+      row[k].owned = slot != kNone || zero;
       row[k].at = (t0 + j) * ts + h * hs + c4 * (D / 4);
       if (slot < 0) continue;
       const int64_t vec = slot + (int64_t(h) << a.log_page);
@@ -347,6 +347,13 @@ __global__ void __launch_bounds__(kThreads, kReadCtas) k_kv_read(const KvArgs a,
   }
 }
 
+// A call without sequences whose rows are to be zero.
+__global__ void __launch_bounds__(kThreads) k_kv_zero(void* out, int64_t tokens, int heads, int row_bytes,
+                                                      int64_t token_bytes, int64_t head_bytes) {
+  kv_zero_rows(out, 0, 0, tokens, heads, row_bytes, token_bytes, head_bytes,
+               int64_t(blockIdx.x) * blockDim.x + threadIdx.x, int64_t(gridDim.x) * blockDim.x);
+}
+
 // Tokens per CTA such that the CTAs that fit the GPU at once (`ctas` on an SM)
 // share them evenly: a CTA finds its tokens' places once and then has the next
 // vectors on their way while it works on these.
@@ -390,6 +397,7 @@ struct Append {
 struct Read {
   const KvArgs& a;
   const KvDense& y;
+  bool zero;
   cudaStream_t st;
   template <int D, int BITS, bool F32>
   cudaError_t go() {
@@ -401,7 +409,7 @@ struct Read {
     const int es = F32 ? 4 : 2;
     const bool wide = (reinterpret_cast<uintptr_t>(y.k) | reinterpret_cast<uintptr_t>(y.v) | uintptr_t(y.k_ts * es) |
                        uintptr_t(y.k_hs * es) | uintptr_t(y.v_ts * es) | uintptr_t(y.v_hs * es)) % 32 == 0;
-    k_kv_read<D, BITS, F32><<<grid, threads, 0, st>>>(a, y, tile, norm_of(D), wide, make_fastdiv(a.hk));
+    k_kv_read<D, BITS, F32><<<grid, threads, 0, st>>>(a, y, tile, norm_of(D), wide, zero, make_fastdiv(a.hk));
     return cudaGetLastError();
   }
 };
@@ -411,8 +419,16 @@ struct Read {
 cudaError_t launch_kv_append(const KvArgs& a, const KvDense& x, int dt, cudaStream_t st) {
   return by_format(a, dt, Append{a, x, st});
 }
-cudaError_t launch_kv_read(const KvArgs& a, const KvDense& y, int dt, cudaStream_t st) {
-  return by_format(a, dt, Read{a, y, st});
+cudaError_t launch_kv_read(const KvArgs& a, const KvDense& y, int dt, bool zero, cudaStream_t st) {
+  return by_format(a, dt, Read{a, y, zero, st});
+}
+cudaError_t launch_kv_zero(void* out, int64_t tokens, int heads, int head_dim, int64_t ts, int64_t hs, int dt,
+                           cudaStream_t st) {
+  const int es = dt == 0 ? 4 : 2;
+  const int64_t pieces = tokens * heads * (head_dim * es / 16);
+  const unsigned grid = unsigned(std::min<int64_t>(148 * 8, (pieces + kThreads - 1) / kThreads));
+  k_kv_zero<<<grid, kThreads, 0, st>>>(out, tokens, heads, head_dim * es, ts * es, hs * es);
+  return cudaGetLastError();
 }
 
 }  // namespace hit

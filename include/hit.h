@@ -370,7 +370,8 @@ HIT_API int harp_blocks(const float* theta, const int8_t* theta_q, float theta_s
  *  - cu: int32 [seqs + 1], ascending; sequence s owns tokens cu[s] <= t <
  *    cu[s+1] of the call (n_s of them, possibly none).  Tokens before cu[0]
  *    and at or behind cu[seqs] belong to no sequence: their inputs are not
- *    used and their outputs are left as they were.
+ *    used and their outputs are left as they were, or set to zero where
+ *    HIT_KV_ZERO is added to dtype_out (rht_kv_read: dtype).
  *  - lens: int32 [seqs], the positions sequence s has, this call's tokens
  *    included: token t has position lens[s] - n_s + (t - cu[s]).
  *  - page_table: int32 [seqs, ld_table], max_pages of each row used; position
@@ -424,6 +425,8 @@ HIT_API int harp_blocks(const float* theta, const int8_t* theta_q, float theta_s
  *   stands for at the call's tokens (rows is the number of tokens; either
  *   output may be NULL).  Keys come back with their rotary turn.
  */
+#define HIT_KV_ZERO 0x100
+
 typedef struct hit_kv {
   uint8_t* k_codes;
   float* k_scales;
