@@ -575,7 +575,10 @@ def rht_kv_attention(q, k_codes, k_scales, v_codes, v_scales, page_table, lens, 
             raise ValueError("out must have q's shape and device")
     kv = _kv(d, dev, n, k_codes, k_scales, v_codes, v_scales, page_table, lens, cu, k_signs, v_signs, inv_freq,
              interleaved, positions, rope_axis)
-    max_new = max(n, 1) if max_new is None else int(max_new)
+    max_new = max(n, 1) if max_new is None else min(int(max_new), 1 << 40)
+    window = min(int(window), 1 << 40)
+    if window < 0 or max_new < 1:
+        raise ValueError("window must not be negative and max_new must be positive")
     if workspace is None:
         size = load().rht_kv_workspace_bytes(n, heads, k_codes.shape[1], d, max_new)
         workspace = torch.empty_strided((size,), (1,), dtype=torch.uint8, device=q.device)
@@ -586,7 +589,7 @@ def rht_kv_attention(q, k_codes, k_scales, v_codes, v_scales, page_table, lens, 
     q_ts, q_hs, _ = q.stride()
     o_ts, o_hs, _ = out.stride()
     _kv_call(dev, "rht_kv_attention", kv, q.data_ptr(), out.data_ptr(), n, heads, q_ts, q_hs, o_ts, o_hs, _dt(q.dtype),
-             _dt(out.dtype) | zero, float(d ** -0.5 if sm_scale is None else sm_scale), int(bool(causal)), int(window), max_new,
+             _dt(out.dtype) | zero, float(d ** -0.5 if sm_scale is None else sm_scale), int(bool(causal)), window, max_new,
              workspace.data_ptr(), size)
     return out
 

@@ -230,7 +230,7 @@ int rht_kv_attention(const hit_kv* kv, const void* q, void* out, int64_t tokens,
   t.zero = zero ? 1 : 0;
   t.causal = causal ? 1 : 0;
   t.scale = sm_scale;
-  t.window = window;
+  t.window = std::min<int64_t>(window, kMaxTokens * 4);  // as good as any longer one, and positions less it stay in 64 bits
   t.max_new = max_new < tokens ? max_new : tokens;
   t.ws = workspace;
   if (few_only(t.max_new, t.group, a.head_dim)) return cuda_status(hit::launch_kv_few(a, t, st), fn);
