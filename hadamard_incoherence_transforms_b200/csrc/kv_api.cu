@@ -4,6 +4,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <cstdlib>
 
 #include "hit.h"
 #include "internal.h"
@@ -120,6 +121,25 @@ int check_dense(const char* fn, const char* name, const void* p, int64_t ts, int
   return HIT_OK;
 }
 
+// Whether two rows of n elements of a [tokens, heads, n] tensor share an element.
+bool rows_overlap(int64_t tokens, int64_t heads, int64_t n, int64_t ts, int64_t hs) {
+  if ((heads > 1 && hs < n) || (tokens > 1 && ts < n)) return true;
+  // a token's heads end before the next token, or a head's tokens before the next head
+  if (heads < 2 || tokens < 2 || (ts - n) / hs >= heads - 1 || (hs - n) / ts >= tokens - 1) return false;
+  for (int64_t h = 1; h < heads; ++h)  // rows (t + a, 0) and (t, h) for the a on both sides of h hs / ts
+    for (int64_t a = h * hs / ts; a <= h * hs / ts + 1 && a < tokens; ++a)
+      if (std::abs(h * hs - a * ts) < n) return true;
+  return false;
+}
+
+// An operand that is written.
+int check_out(const char* fn, const char* name, const void* p, int64_t tokens, int64_t heads, int64_t n, int64_t ts,
+              int64_t hs, int dt) {
+  const int r = check_dense(fn, name, p, ts, hs, dt);
+  if (r == HIT_OK && rows_overlap(tokens, heads, n, ts, hs)) return fail(HIT_EINVAL, "%s: rows of %s overlap", fn, name);
+  return r;
+}
+
 }  // namespace
 
 extern "C" {
@@ -156,8 +176,8 @@ int rht_kv_read(const hit_kv* kv, void* k, void* v, int64_t rows, int64_t k_ts, 
   int r = check_kv(fn, kv, rows, false, a);
   if (r) return r;
   if (rows == 0 || (a.seqs == 0 && !zero) || (k == nullptr && v == nullptr)) return HIT_OK;
-  if (k != nullptr && (r = check_dense(fn, "k", k, k_ts, k_hs, dtype)) != 0) return r;
-  if (v != nullptr && (r = check_dense(fn, "v", v, v_ts, v_hs, dtype)) != 0) return r;
+  if (k != nullptr && (r = check_out(fn, "k", k, rows, a.hk, a.head_dim, k_ts, k_hs, dtype)) != 0) return r;
+  if (v != nullptr && (r = check_out(fn, "v", v, rows, a.hk, a.head_dim, v_ts, v_hs, dtype)) != 0) return r;
   hit::KvDense y;
   y.k = k;
   y.v = v;
@@ -204,7 +224,7 @@ int rht_kv_attention(const hit_kv* kv, const void* q, void* out, int64_t tokens,
   if (tokens * heads >= kMaxTokens) return fail(HIT_EUNSUPPORTED, "%s: tokens * heads must stay below 2^31", fn);
   r = check_dense(fn, "q", q, q_ts, q_hs, dtype_q);
   if (r) return r;
-  r = check_dense(fn, "out", out, o_ts, o_hs, dtype_out);
+  r = check_out(fn, "out", out, tokens, heads, a.head_dim, o_ts, o_hs, dtype_out);
   if (r) return r;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (a.seqs == 0) return cuda_status(hit::launch_kv_zero(out, tokens, heads, a.head_dim, o_ts, o_hs, dtype_out, st), fn);

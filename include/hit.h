@@ -405,7 +405,8 @@ HIT_API int harp_blocks(const float* theta, const int8_t* theta_q, float theta_s
  *   sm_scale * (R_k rope(q[t, h])) . (stored key j).  A token at position p
  *   sees j < lens[s], with causal != 0 only j <= p, and with window > 0 (causal
  *   only) only j > p - window.  A token that sees nothing gets 0.  q, out:
- *   [tokens, heads, head_dim], strided as k.  Arithmetic: queries (behind a
+ *   [tokens, heads, head_dim], strided as k (rows of out must not overlap; it may
+ *   be q's own memory, with q's type and strides).  Arithmetic: queries (behind a
  *   power of two of their own row) fp16, scores and outputs summed in fp32,
  *   softmax in fp32.  Where a sequence has at most 64 query rows (tokens * heads
  *   / kv_heads; 32 with head_dim 256) for a key/value head, codes and the keys'
@@ -423,7 +424,8 @@ HIT_API int harp_blocks(const float* theta, const int8_t* theta_q, float theta_s
  *   which calls that may run at the same time must not share.
  * rht_kv_read: k, v [rows, kv_heads, head_dim] <- R^-1 of what the cache
  *   stands for at the call's tokens (rows is the number of tokens; either
- *   output may be NULL).  Keys come back with their rotary turn.
+ *   output may be NULL; rows of an output must not overlap).  Keys come back
+ *   with their rotary turn.
  */
 #define HIT_KV_ZERO 0x100
 
