@@ -68,7 +68,7 @@ def over_root_mean_square(err, want, square, score, is_few, out_dtype):
 
 @pytest.mark.parametrize("new,g", FORMS)
 @pytest.mark.parametrize("d,bits", SIZES)
-@pytest.mark.parametrize("sharp", [0.1, 1.0])
+@pytest.mark.parametrize("sharp", [0.1, 0.7])
 @pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
 def test_error_of_the_whole_result(new, g, d, bits, sharp, out_dtype):
     """Roundings are independent and at most u, so their root mean square is at most u / sqrt(3).  A row's error is the sum
