@@ -182,6 +182,18 @@ __device__ __forceinline__ void kv_times(float (&x)[32], const float* f, int l) 
   }
 }
 
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// max that keeps a NaN
+__device__ __forceinline__ float kv_max(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // The power of two of a row whose largest absolute element has the bits m, and
 // its reciprocal; 1 for an infinity or a NaN, which are left to spread.
 __device__ __forceinline__ void kv_row_power(uint32_t m, float& up, float& down) {

@@ -436,11 +436,6 @@ template <int N>
 __device__ __forceinline__ void regs_less() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 
 // One row's softmax of a unit: its 128 scores in tensor memory become
 // probabilities (fp16, in the same place).  m: the reference they are relative

@@ -192,12 +192,6 @@ __device__ __forceinline__ void kv_finish(float (&x)[D / 32], const KvArgs& a, c
 // reference or sum stays NaN.  Taken twice, so that a part's sum outlives a weight below
 // 2^-126: references follow the values' sizes too.
 __device__ __forceinline__ float kv_weight(float m, float top) { return m == -INFINITY ? 0.0f : exp2f(0.5f * (m - top)); }
-// max that keeps a NaN
-__device__ __forceinline__ float kv_max(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 
 // Joins the parts of the pairs that several CTAs share: block c handles the
 // pair that CTA c began and did not end (slot 2 c + 1), rows PER y ... of it.  A

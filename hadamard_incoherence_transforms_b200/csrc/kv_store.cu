@@ -19,26 +19,19 @@ constexpr int kThreads = 256;
 constexpr int kMaxTile = 64;  // tokens per CTA
 constexpr int kAppendCtas = 2, kReadCtas = 2;  // CTAs on an SM
 
-// max that keeps a NaN
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
 // Stored codes of the vector x and its scale.  All LPV lanes of the vector call it
-// together.  The usual case takes t = y / s by the correctly rounded quotient:
-// q0 = y r with r = RN(1/s), one correction step (exact remainder), and the code in
-// the low byte of t + 1.5 * 2^23 + 2^(b-1) (ties to even), on pairs.
+// together.  The usual case takes t = y / s by Markstein's correctly rounded
+// quotient, as rows_ops.cuh does: q0 = y r with r = RN(1/s), one correction step (exact
+// remainder), and the code in the low byte of t + 1.5 * 2^23 + 2^(b-1) (ties to even), on pairs.
 template <int D, int BITS>
 __device__ __forceinline__ float kv_quantize(float (&x)[32], uint32_t (&w)[BITS]) {
   constexpr int QMAX = (1 << (BITS - 1)) - 1;
   constexpr float MAGIC = 12582912.0f + float(1 << (BITS - 1));
   float a = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) a = max_nan(a, fabsf(x[i]));
+  for (int i = 0; i < 32; ++i) a = kv_max(a, fabsf(x[i]));
 #pragma unroll
-  for (int b = 0; b < KvLanes<D>::LOG; ++b) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, 1 << b));
+  for (int b = 0; b < KvLanes<D>::LOG; ++b) a = kv_max(a, __shfl_xor_sync(0xffffffffu, a, 1 << b));
   float s = __fdiv_rn(a, float(QMAX));
   if (!(a < INFINITY)) s = __uint_as_float(0x7fc00000u);
   uint32_t u[32];
