@@ -44,8 +44,13 @@ constexpr int kThreads = 16 * 32;  // warps 14 and 15 are idle: registers are de
 constexpr int kCtas = 148;
 constexpr float kGrow = 32768.0f;  // sum of 32 probabilities above which a row gets a new reference
 constexpr float kRoom = 4.0f;      // a reference's own probability is 2^kRoom
-constexpr int kValueBits = 4;      // the largest scale of the unit that a power of two was taken from becomes 2^kValueBits or more
-constexpr int kSpread = 8;         // scales down to 2^-kSpread of the largest share its power of two
+constexpr int kKeyBits = 7;        // the largest key scale of a unit becomes 2^kKeyBits or more
+constexpr int kValueBits = 4;      // the largest value scale of the unit that a power of two was taken from, 2^kValueBits
+// Scales down to 2^-kKeySpread and 2^-kValueSpread of the largest share its power of two: the
+// second part of a scale still is 2^-16 of it there.  A block with a scale below that takes
+// nine times as long (UnitSoftmax::run_apart); the values of first tokens that everything
+// attends to are about 2^-7 of the others.
+constexpr int kKeySpread = 16, kValueSpread = 12;
 
 template <int D>
 struct Prompt {
@@ -1118,10 +1123,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
           // with a scale in two parts, hi and the rest.  Keys are relative to a
           // power of two of the unit's largest scale, so that fp16 holds them, values
           // to one of the largest scale of a unit before while that of this one is at most
-          // 2^3 times as large and no less than 2^-5 of it (else its own, and O is brought to
-          // it).  Codes times scales then stay below 2^15 and keep 11 bits down to
-          // 2^-kSpread (bf16 values cost the result 2^-8 of each, 0.0029 in place of 0.0017
-          // in all).  A position whose scale is smaller takes its own power of two, which
+          // 2^3 times as large and no less than 2^-6 of it (else its own, and O is brought to
+          // it).  Codes times scales then stay below 2^15 and keep 11 bits (bf16 values cost
+          // the result 2^-8 of each, 0.0029 in place of 0.0017 in all).  A position whose scale is smaller takes its own power of two, which
           // the softmax multiplies in (UnitSoftmax::run_apart): else one large scale,
           // hidden or not, would leave the others no digits.  A position whose scale is not
           // finite becomes NaN in its scores, and only there.
@@ -1144,23 +1148,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
           int kex = 0;  // exponent of the unit's largest key scale
           if constexpr (KEYS) {
             const uint4 all = *reinterpret_cast<const uint4*>(tops);
-            kex = int(max(1u, max(max(all.x, all.y), max(all.z, all.w)) >> 23));
+            kex = int(max(8u, max(max(all.x, all.y), max(all.z, all.w)) >> 23));
             told = kex > 255;
-            if (i == 0) *reinterpret_cast<uint32_t*>(scp + 16) = uint32_t(kex) << 23;
+            if (i == 0) *reinterpret_cast<uint32_t*>(scp + 16) = uint32_t(kex - kKeyBits) << 23;
           }
           if constexpr (VALUES) {
             const uint4 all = *reinterpret_cast<const uint4*>(tops + 4);
             const uint32_t vtop = max(max(all.x, all.y), max(all.z, all.w)) >> 23;
             told = vtop > 255;
             const int vx = max(8, int(vtop));
-            if (j == ub || vx > vex + 3 || (vtop != 0 && vx < vex - 5)) vex = vx;
+            if (j == ub || vx > vex + 3 || (vtop != 0 && vx < vex - 6)) vex = vx;
             if (i == 0) *reinterpret_cast<uint32_t*>(scp + 20) = uint32_t(vex - kValueBits);
           }
           if (told) break;
           const int k_own = int(__float_as_uint(ksc) >> 23) & 255, v_own = int(__float_as_uint(vsc) >> 23) & 255;
-          const bool k_apart = KEYS && k_own + kSpread < kex && ksc != 0.0f;
-          const bool v_apart = VALUES && v_own + kSpread < vex && vsc != 0.0f;
-          const int ke = k_apart ? max(1, k_own) : kex, ve = v_apart ? max(1, v_own) : vex - kValueBits;
+          const bool k_apart = KEYS && k_own + kKeySpread < kex && ksc != 0.0f;
+          const bool v_apart = VALUES && v_own + kValueSpread < vex && vsc != 0.0f;
+          const int ke = k_apart ? max(1, k_own) : kex - kKeyBits, ve = v_apart ? max(1, v_own) : vex - kValueBits;
           uint32_t k_hi, k_lo, v_hi, v_lo;
           {
             auto inverse = [](int e) { return __uint_as_float(e == 254 ? 0x00400000u : uint32_t(254 - e) << 23); };

@@ -25,9 +25,10 @@ def set_scale(c, which, s, positions, value, code=None):
 def attention(q, c, cu, window):
     """Causal attention in float64, and for every row sum p |v| and the sum that a unit of relative error of the scores
     costs: a probability off by p_j (e_j - sum p e), e_j = sum_i |q_i k_ji|, moves the result by at most
-    sum_j p_j e_j |v_j| + (sum p e) (sum p |v|)."""
+    sum_j p_j e_j |v_j| + (sum p e) (sum p |v|).  Last, what is lost where fp16 holds probabilities whose largest is 2^4
+    or more: 2^-25 of each, or all of a smaller one."""
     tokens, n, _ = q.shape
-    want, value, spread = np.zeros(q.shape), np.zeros((tokens, n)), np.zeros((tokens, n))
+    want, (value, spread, lost) = np.zeros(q.shape), (np.zeros((tokens, n)) for _ in range(3))
     x = kc.rotate(q, c.k_signs) * c.d ** -0.5
     for s, length in enumerate(c.lens):
         t = np.arange(cu[s], cu[s + 1])
@@ -43,19 +44,21 @@ def attention(q, c, cu, window):
             want[t, h] = kc.unrotate(p @ v, c.v_signs)
             value[t, h] = p @ size
             spread[t, h] = (p * e) @ size + (p * e).sum(1) * value[t, h]
-    return want, value, spread
+            lost[t, h] = np.minimum(p, 2.0 ** -29 * p.max(1, keepdims=True)) @ size
+    return want, value, spread, lost
 
 
 def check_rows(got, ref, rows, positions):
     """fp32 results of the rows within the worst case of the roundings.  Query and key are rounded to fp16, u_h each: a
-    score is off by 2 u_h sum|q k|.  Probability and value are rounded to fp16, u_h each.  A probability (times its value's
-    scale) below fp16's normal range is off by 2^-25 where the row's largest is 2^4 or more, and scales of a block that are
-    worked on together lie within 2^12: 2^-17 for a position.  fp32 sums: 2^-14."""
-    want, value, spread = (x[rows] for x in ref)
+    score is off by 2 u_h sum|q k|.  Probability and value are rounded to fp16, u_h each, and below fp16's normal
+    range a probability loses what `lost` counts, a product of probability and scale (few rows) 2^-29 of the row's
+    largest.  fp32 sums: 2^-14."""
+    want, value, spread, lost = (x[rows] for x in ref)
     got = got.double().cpu().numpy()[rows]
     assert np.isfinite(want).all() and np.isfinite(got).all()
     err = np.linalg.norm(got - want, axis=-1)
-    bound = 2 * UH * spread + (2 * UH + 2.0 ** -14 + positions * 2.0 ** -17) * value + U32 * np.linalg.norm(want, axis=-1)
+    bound = 2 * UH * spread + (2 * UH + 2.0 ** -14 + positions * 2.0 ** -29) * value + lost
+    bound += U32 * np.linalg.norm(want, axis=-1)
     assert (err <= bound).all(), f"{(err / np.maximum(bound, 1e-300)).max():.2f} of the bound"
 
 
@@ -187,3 +190,19 @@ def test_values_that_go_up_and_down_by_blocks(new, g, d, bits, steps, light):
                 c.k[1][page, :, k] = float(w[0]) * 60 / -worst
     got, ref = run(c, [new], g, q64=q64)
     check_rows(got, ref, np.arange(new), 128 * len(steps) + 100)
+
+
+@pytest.mark.parametrize("d,bits", SIZES)
+@pytest.mark.parametrize("down", [6, 9, 14, 18])
+def test_prompts_with_a_first_token_of_small_values(d, bits, down):
+    """A first position with most of the weight and values 2^-6 to 2^-18 of the others'."""
+    c = Cache(97, [600], 1, d, bits, 16).fill()
+    x = c.r.randn(d)
+    q64 = 0.2 * c.r.randn(100, 2, d) + x
+    code, w, _ = kc.quantize(kc.rotate(x, c.k_signs)[None], bits)
+    page, i = kc.slot(c.table, c.pages, c.page, 0, 0)
+    c.k[0][page, :, i] = kc.pack(code, bits)[0]
+    c.k[1][page, :, i] = w
+    c.v[1][page, :, i] *= 2.0 ** -down
+    got, ref = run(c, [100], 2, q64=q64)
+    check_rows(got, ref, np.arange(100), 600)
