@@ -562,7 +562,8 @@ def rht_kv_attention(q, k_codes, k_scales, v_codes, v_scales, page_table, lens, 
 
     q is turned and rotated as the keys were; the result is rotated back.  A token at position p sees the cached
     positions up to p (all of them with causal=False; the last `window` ones with window > 0).  max_new bounds the
-    tokens of one sequence (default: all of them).  out may be float32 or bfloat16 (default: q's type).  Rows of tokens
+    tokens of one sequence.  Give it where there are several sequences: by default it is all tokens of the call, and a
+    batch of single tokens then takes the launches of a long chunk.  out may be float32 or bfloat16 (default: q's type).  Rows of tokens
     that belong to no sequence (before cu[0], from cu[-1] on) are zero, or as they were where out is given."""
     _kv_dense(q, "q")
     dev, (n, heads, d) = q.get_device(), q.shape

@@ -34,10 +34,12 @@ constexpr int64_t kMaxTokens = int64_t(1) << 31;
 // Sequences with up to kFewRows query rows for a key/value head go to the kernel
 // that streams the codes once for 16 rows (an SM takes 7 cycles for a position and
 // 16 rows), the others to the one that works on 256 rows at a time (40 cycles for a
-// position, whatever the rows).  Heads of 256 go 8 and 128 rows at a time: 64
-// sequences of 16 rows take 260 us and 452, of 32 rows 474 and 408, of 64 rows 939
-// and 427; two sequences of 25 rows 32 and 53.  Each launch leaves the other's
-// sequences alone, so that max_new decides only whether the second kind is needed.
+// position, whatever the rows).  64 sequences of up to 4,000 positions take 216 us and
+// 277 with 32 rows, 414 and 283 with 64, 849 and 324 with 128; a call of few sequences
+// gains more from the first kind's one launch.  Heads of 256 go 8 and 128 rows at a time:
+// 233 and 345 us with 16 rows, 425 and 348 with 32, 848 and 359 with 64; two sequences of
+// 25 rows 32 and 50.  Each launch leaves the other's sequences alone, so that max_new
+// decides only whether the second kind is needed.
 constexpr int64_t kFewRows = 64, kFewRows256 = 32;
 int64_t few_rows(int head_dim) { return head_dim == 256 ? kFewRows256 : kFewRows; }
 bool few_only(int64_t max_new, int64_t group, int head_dim) { return max_new * group <= few_rows(head_dim); }

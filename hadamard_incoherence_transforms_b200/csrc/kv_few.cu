@@ -22,7 +22,7 @@
 // score, the value's its probability.
 //
 // 64 sequences of 300 to 8,000 positions (32 heads on 8, head 128, 4 bits) take
-// 84 us, two of 125,000 (8 bits) 70 us: 3.0 and 3.9 TB/s, where the loop over the
+// 85 us, two of 125,000 (8 bits) 69 us: 3.0 and 4.0 TB/s, where the loop over the
 // units alone runs at 5.3 to 5.9 TB/s.  The rest is finding the share, preparing
 // the queries and the first loads (about 10 us), uneven ends, and the joining
 // launch (8 us).

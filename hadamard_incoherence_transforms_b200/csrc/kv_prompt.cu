@@ -14,15 +14,19 @@
 // The two halves alternate: while one half's softmax runs, the tensor cores
 // work on the other's products.  Key and value units are converted once for
 // both, their scales folded in with one rounding of 2^-11 (half the work of the
-// softmax roles went into scales otherwise, see UnitSoftmax for what is left).
+// softmax roles went into scales otherwise, see UnitSoftmax for what is left) wherever a
+// block's scales lie within 2^kSpread of one another.
 //
-// 4,096 tokens on 12,000 cached ones (32 heads on 8, head 128, 4 bits) take 1.24 ms,
-// 760 TFLOP/s or 46 % of a measured library product; 8 bits 1.45 ms.  A unit takes
-// 5,600 cycles: a half's softmax 3,400 of them (1,500 were it alone on the SM; both
-// halves share the exponential units, 2,048 a unit), and 2,200 until its next scores
-// are there (products of both halves, 2,050 a unit at the pipe's rate).  Scores in
-// two parts of 64 positions, the next one's product under way during the softmax,
-// took 1.30 ms: products of 64 columns read the queries from shared memory twice.
+// 4,096 tokens on 12,000 cached ones (32 heads on 8, head 128, 4 bits) take 1.27 ms,
+// 742 TFLOP/s or 44 % of a measured library product; 8 bits 1.44 ms.  Before positions could
+// have powers of two of their own it was 1.23 ms; of the 0.04 the unpacking warps'
+// tests of each scale are 0.03.  A unit took 5,600 cycles then: a half's softmax 3,400 of
+// them (1,500 were it alone on the SM; both halves share the exponential units, 2,048 a
+// unit), and 2,200 until its next scores are there (products of both halves, 2,050 a
+// unit at the pipe's rate).  Scores in two parts of 64 positions, the next one's product
+// under way during the softmax, took 1.30 ms against 1.24: products of 64 columns read the
+// queries from shared memory twice.  Heads of 64 and 128 spill 300 to 440 bytes a thread
+// (-Xptxas -v; heads of 256 none to speak of); what that costs is not known.
 #include "internal.h"
 #include "kv_codes.cuh"
 #include "kv_split.cuh"
@@ -1063,8 +1067,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
     regs_less<F::UNPACK>();
     const int i = threadIdx.x & 127;
     // keys and values by the same threads, or (heads of 256) the values by warps 4-7:
-    // 1,024 tokens on 12,000 (32 heads on 8) take 706 us with 8 bits and 660 with 4; with
-    // one group 1,010 and 674
+    // 1,024 tokens on 12,000 (32 heads on 8) take 730 us with 8 bits and 695 with 4 (706 and
+    // 660, with one group 1,010 and 674, before positions had powers of two of their own)
     auto unpack = [&](auto keys_too, auto values_too) {
       constexpr bool KEYS = decltype(keys_too)::value, VALUES = decltype(values_too)::value;
       uint32_t kv = 0;
