@@ -563,8 +563,9 @@ def rht_kv_attention(q, k_codes, k_scales, v_codes, v_scales, page_table, lens, 
     q is turned and rotated as the keys were; the result is rotated back.  A token at position p sees the cached
     positions up to p (all of them with causal=False; the last `window` ones with window > 0).  max_new bounds the
     tokens of one sequence.  Give it where there are several sequences: by default it is all tokens of the call, and a
-    batch of single tokens then takes the launches of a long chunk.  out may be float32 or bfloat16 (default: q's type).  Rows of tokens
-    that belong to no sequence (before cu[0], from cu[-1] on) are zero, or as they were where out is given."""
+    batch of single tokens then takes the launches of a long chunk.  out may be float32 or bfloat16 (default: q's
+    type).  Rows of tokens that belong to no sequence (before cu[0], from cu[-1] on) are zero, or as they were where
+    out is given."""
     _kv_dense(q, "q")
     dev, (n, heads, d) = q.get_device(), q.shape
     zero = 0
@@ -576,10 +577,9 @@ def rht_kv_attention(q, k_codes, k_scales, v_codes, v_scales, page_table, lens, 
             raise ValueError("out must have q's shape and device")
     kv = _kv(d, dev, n, k_codes, k_scales, v_codes, v_scales, page_table, lens, cu, k_signs, v_signs, inv_freq,
              interleaved, positions, rope_axis)
-    max_new = max(n, 1) if max_new is None else min(int(max_new), 1 << 40)
-    window = min(int(window), 1 << 40)
-    if window < 0 or max_new < 1:
-        raise ValueError("window must not be negative and max_new must be positive")
+    # numbers of any size reach the library as ones of 64 bits with the same meaning
+    max_new = max(n, 1) if max_new is None else max(0, min(int(max_new), 1 << 40))
+    window = max(-1, min(int(window), 1 << 40))
     if workspace is None:
         size = load().rht_kv_workspace_bytes(n, heads, k_codes.shape[1], d, max_new)
         workspace = torch.empty_strided((size,), (1,), dtype=torch.uint8, device=q.device)

@@ -51,9 +51,9 @@ constexpr float kRoom = 4.0f;      // a reference's own probability is 2^kRoom
 constexpr int kKeyBits = 7;        // the largest key scale of a unit becomes 2^kKeyBits or more
 constexpr int kValueBits = 4;      // the largest value scale of the unit that a power of two was taken from, 2^kValueBits
 // Scales down to 2^-kSpread of the largest share its power of two: the second part of a scale
-// is 2^-16 (keys) and 2^-12 (values) of it there, or more.  A block with a scale below that takes nine times
-// as long (UnitSoftmax::run_apart): values drawn over 2^14 in every block take 1.27 ms
-// with 16 and 10.6 with 12.
+// is 2^-16 (keys) and 2^-12 (values) of it there, or more.  A block with a scale below that
+// takes nine times as long (UnitSoftmax::run_apart): values' scales drawn over 2^10 from
+// position to position, beside their usual spread, take 1.28 ms with 16 and 10.6 with 12.
 constexpr int kSpread = 16;
 
 template <int D>
@@ -464,7 +464,7 @@ struct UnitSoftmax {
   int c_lo, c_hi;       // columns [c_lo, c_hi) are this row's
   float qu;             // the row's and the unit's power of two
 
-  // The same for a unit some of whose scales lie so far below the largest that their
+  // The softmax of a unit some of whose scales lie so far below the largest that their
   // keys or values are held by powers of two of their own (own: their exponents, keys' ahead
   // of values'; 0 where it is the unit's).  Scores are multiplied by the keys',
   // and probabilities (not their sum) by the values', relative to a power of two
@@ -1129,10 +1129,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_prompt(const KvArgs a, const
           // to one of the largest scale of a unit before while that of this one is at most
           // 2^3 times as large and no less than 2^-6 of it (else its own, and O is brought to
           // it).  Codes times scales then stay below 2^15 and keep 11 bits (bf16 values cost
-          // the result 2^-8 of each, 0.0029 in place of 0.0017 in all).  A position whose scale is smaller takes its own power of two, which
-          // the softmax multiplies in (UnitSoftmax::run_apart): else one large scale,
-          // hidden or not, would leave the others no digits.  A position whose scale is not
-          // finite becomes NaN in its scores, and only there.
+          // the result 2^-8 of each, 0.0029 in place of 0.0017 in all).  A position whose
+          // scale is smaller by more than 2^kSpread takes its own power of two, which the
+          // softmax multiplies in (UnitSoftmax::run_apart): else one large scale, hidden or
+          // not, would leave the others no digits.  A position whose scale is not finite
+          // becomes NaN in its scores, and only there.
           uint32_t* const tops = reinterpret_cast<uint32_t*>(smem + F::TS + (kv & 1) * 32);
           uint8_t* const scp = smem + F::SC + (kv & 3) * F::SC_STAGE;
           uint8_t* const apart = scp + (KEYS ? 24 : 28) + (warp & 3);  // whether a position of this warp's is
